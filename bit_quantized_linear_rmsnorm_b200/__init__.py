@@ -34,6 +34,7 @@ EXPORTED = [
     "bq_workspace_bytes",
     "bq_bitlinear_workspace_layout", "bq_status_string", "bq_device_status", "bq_version",
     "bq_bitlinear_w2a8_noalloc", "bq_bitlinear_w2a8_path", "bq_diag_gemm_withheld_arrival",
+    "bq_kv4_page_bytes", "bq_kv4_write", "bq_kv4_read", "bq_kv4_attention", "bq_kv4_attention_workspace_bytes",
 ]
 (BQ_PATH_DECODE_STREAM, BQ_PATH_DECODE_MMA, BQ_PATH_DECODE_SMEM, BQ_PATH_ACT_QUANT_GEMV, BQ_PATH_TC_SINGLE,
  BQ_PATH_TC_PAIR) = range(1, 7)
@@ -75,6 +76,13 @@ _SIGS = {
     "bq_status_string": (ctypes.c_char_p, [I32]),
     "bq_device_status": (I32, [P, ctypes.POINTER(ctypes.c_uint32)]),
     "bq_version": (I32, []),
+    "bq_kv4_page_bytes": (SZ, [I64, I64, I64]),
+    "bq_kv4_write": (I32, [P, P, I32, I64, I64, I64, I64, I64, I64, I64, P, P, I64, P, I64, I64, P, I64, I64, I64, I64,
+                           P]),
+    "bq_kv4_read": (I32, [P, I64, I64, I64, I64, I64, I64, P, I64, I64, P, P, I64, I64, I32, P, P, P]),
+    "bq_kv4_attention_workspace_bytes": (SZ, [I64, I64, I64, I64]),
+    "bq_kv4_attention": (I32, [P, I32, I64, I64, I64, I64, I64, P, I64, P, I64, P, I64, I64, P, I64, I64, I64, I64, I64,
+                               F32, I64, F32, P, P, P, P, SZ, P]),
 }
 
 _lib = None
@@ -449,3 +457,138 @@ def bq_linear_w4a4_backward(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor
                                        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "bq_linear_w4a4_backward")
     return dx, dw, dscale_a
+
+
+def bq_kv4_page_bytes(page_size: int, head_dim: int, group_size: int) -> int:
+    """Bytes of one (page, head) block of a 4-bit key/value cache (0: sizes that are not supported)."""
+    return int(lib().bq_kv4_page_bytes(page_size, head_dim, group_size))
+
+
+def _kv4_cache(cache: torch.Tensor, D: int, group_size: int, *tables):
+    """(pages, page stride, page size, heads) of a cache [pages, kv_heads, page_bytes], after checking it and the
+    int32 tables that go with it (None: not given)."""
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or group_size < 1 or D % group_size != 0:
+        raise ValueError("expected a uint8 cache [pages, kv_heads, page_bytes] and a group_size that divides head_dim")
+    pages, H, nbytes = cache.shape
+    page = nbytes // (D + 8 * (D // group_size))
+    if page * (D + 8 * (D // group_size)) != nbytes or (pages and (cache.stride(2) != 1 or
+                                                                   (H > 1 and cache.stride(1) != nbytes))):
+        raise ValueError("the cache's last two dimensions must be dense, of bq_kv4_page_bytes() bytes per head")
+    for t in tables:
+        if t is not None and (t.dtype != torch.int32 or t.device != cache.device or
+                              (t.stride(-1) != 1 and t.shape[-1] > 1)):
+            raise ValueError("block_table, lengths and offsets must be int32 on the cache's device, dense along a row")
+    return pages, (cache.stride(0) if pages > 1 else H * nbytes), page, H
+
+
+def _kv4_ld(table: torch.Tensor) -> int:
+    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+
+
+def _kv4_batch(block_table, lens, cu, starts=None):
+    """Number of sequences, after checking that the tables agree on it."""
+    if block_table.dim() != 2:
+        raise ValueError("expected a block_table [batch, pages of a sequence]")
+    B = block_table.shape[0]
+    if (lens is not None and lens.shape != (B,)) or (cu is not None and cu.shape != (B + 1,)) or \
+            (starts is not None and starts.shape != (B,)):
+        raise ValueError("lengths [batch] and offsets [batch + 1] must match block_table [batch, ...]")
+    return B
+
+
+def _step(t: torch.Tensor, dim: int) -> int:
+    """Stride of a dimension that is walked along (that of a dimension of one element is anything)."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _kv4_call(device, call, stream):
+    """call(stream handle) with `device` current (the library launches on the current device)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream() if stream is None else stream
+        return call(s.cuda_stream)
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream() if stream is None else stream
+        return call(s.cuda_stream)
+
+
+def bq_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, group_size: int, cu_q=None, stream=None):
+    """Quantizes new key and value rows [T, kv_heads, D] into their pages of `cache` (uint8 [pages, kv_heads,
+    page_bytes]); returns the cache.  seq_lens counts the rows written; cu_q [batch + 1] gives the rows of each
+    sequence (None: T / batch each)."""
+    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.device != cache.device or \
+            v.device != cache.device or (k.numel() and (k.stride(2) != 1 or v.stride(2) != 1)):
+        raise ValueError("expected k and v [T, kv_heads, D] of one type, dense along D, on the cache's device")
+    T, H, D = k.shape
+    pages, pstride, page, Hc = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
+    if H != Hc or k.dtype not in _DTYPE:
+        raise ValueError("k and v must have the cache's heads and a supported type")
+    B = _kv4_batch(block_table, seq_lens, cu_q)
+    st = _kv4_call(cache.device, lambda s: lib().bq_kv4_write(
+        k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], T, H, D, _step(k, 0), _step(k, 1), _step(v, 0), _step(v, 1),
+        None if cu_q is None else cu_q.data_ptr(), seq_lens.data_ptr(), B, block_table.data_ptr(),
+        _kv4_ld(block_table), block_table.shape[1], cache.data_ptr(), pages, pstride, page, group_size, s), stream)
+    _check(st, "bq_kv4_write")
+    return cache
+
+
+def bq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Tensor, total: int, head_dim: int,
+                group_size: int, starts=None, out_dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """(k, v) [total, kv_heads, D]: positions starts[b] + j (starts None: 0) of each sequence, its rows cu_len[b] up
+    to cu_len[b + 1]."""
+    pages, pstride, page, H = _kv4_cache(cache, head_dim, group_size, block_table, cu_len, starts)
+    B = _kv4_batch(block_table, None, cu_len, starts)
+    shape = (total, H, head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
+    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.dtype not in _DTYPE or \
+            not (k.is_contiguous() and v.is_contiguous()) or k.device != cache.device or v.device != cache.device:
+        raise ValueError("k and v must be dense [total, kv_heads, head_dim] of one type on the cache's device")
+    st = _kv4_call(cache.device, lambda s: lib().bq_kv4_read(
+        cache.data_ptr(), pages, pstride, page, H, head_dim, group_size, block_table.data_ptr(), _kv4_ld(block_table),
+        block_table.shape[1], None if starts is None else starts.data_ptr(), cu_len.data_ptr(), B, total,
+        _DTYPE[k.dtype], k.data_ptr(), v.data_ptr(), s), stream)
+    _check(st, "bq_kv4_read")
+    return k, v
+
+
+def bq_kv4_attention_workspace_bytes(total: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().bq_kv4_attention_workspace_bytes(total, q_heads, kv_heads, head_dim))
+
+
+def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     group_size: int, cu_q=None, max_q=None, scale=None, window: int = 0, softcap: float = 0.0,
+                     slopes=None, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of q [T, q_heads, D] over a 4-bit cache: each sequence's rows stand at the end of its
+    seq_lens tokens.  cu_q [batch + 1] gives the rows of each sequence (None: T / batch each), max_q the most rows of
+    one (None: T).  Returns out [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given."""
+    if q.dim() != 3 or q.device != cache.device or q.dtype not in _DTYPE or (q.numel() and q.stride(2) != 1):
+        raise ValueError("expected q [T, q_heads, D], dense along D, on the cache's device")
+    T, Hq, D = q.shape
+    pages, pstride, page, H = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
+    B = _kv4_batch(block_table, seq_lens, cu_q)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError("out must be dense, of q's shape, type and device")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (Hq,) or slopes.device != q.device or
+                               not slopes.is_contiguous()):
+        raise ValueError("slopes must be dense fp32 [q_heads] on q's device")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or lse.device != q.device or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be dense fp32 [T, q_heads] on q's device")
+    if workspace is None:
+        workspace = torch.empty(bq_kv4_attention_workspace_bytes(T, Hq, H, D), dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be dense and on q's device")
+    st = _kv4_call(cache.device, lambda s: lib().bq_kv4_attention(
+        q.data_ptr(), _DTYPE[q.dtype], T, Hq, D, _step(q, 0), _step(q, 1), None if cu_q is None else cu_q.data_ptr(),
+        T if max_q is None else max_q, seq_lens.data_ptr(), B, block_table.data_ptr(), _kv4_ld(block_table),
+        block_table.shape[1], cache.data_ptr(), pages, pstride, page, H, group_size,
+        D ** -0.5 if scale is None else scale, window, softcap, None if slopes is None else slopes.data_ptr(),
+        out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), s), stream)
+    _check(st, "bq_kv4_attention")
+    return out

@@ -127,6 +127,56 @@ BitlinearLayout bitlinear_layout(int64_t M, int64_t N, int64_t K) {
     return l;
 }
 
+// ---- 4-bit key/value cache
+bool kv4_sizes_ok(int64_t page_size, int64_t head_dim, int64_t group_size) {
+    return (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128) &&
+           (head_dim == 64 || head_dim == 128) && (group_size == 64 || group_size == 128) && group_size <= head_dim;
+}
+constexpr int64_t kMaxKvHeads = 4096;
+constexpr int64_t kMaxQHeads = 65536;
+
+// Checks what the three calls share and fills the pool and the sequences.
+// `ends` is cu_q (or cu_len); *empty: a valid call with nothing to do.
+bq_status kv4_check(const void *pool, int64_t pages, int64_t page_stride, int64_t page_size, int64_t kv_heads,
+                    int64_t head_dim, int64_t group_size, const int32_t *block_table, int64_t table_ld,
+                    int64_t table_width, const int32_t *ends, const int32_t *lens, int64_t batch, int64_t total,
+                    Kv4Pool *p, Kv4Seqs *s, bool *empty) {
+    *empty = false;
+    if (total < 0 || batch < 0 || pages < 0 || kv_heads < 1 || table_width < 0 || table_ld < table_width ||
+        head_dim < 1 || group_size < 1 || page_size < 1)
+        return BQ_ERR_INVALID_ARG;
+    if (!kv4_sizes_ok(page_size, head_dim, group_size) || kv_heads > kMaxKvHeads || total > kMaxDim ||
+        batch > kMaxDim - 1 || pages > kMaxDim || table_width > kMaxDim)
+        return BQ_ERR_UNSUPPORTED;
+    const int64_t block = static_cast<int64_t>(bq_kv4_page_bytes(page_size, head_dim, group_size));
+    if (page_stride < block * kv_heads) return BQ_ERR_INVALID_ARG;
+    if (page_stride % 16 != 0) return BQ_ERR_MISALIGNED;
+    if (total == 0 || batch == 0) {
+        *empty = true;
+        return BQ_OK;
+    }
+    if (ends == nullptr && total % batch != 0) return BQ_ERR_INVALID_ARG;
+    if ((pool == nullptr && pages > 0) || (block_table == nullptr && table_width > 0)) return BQ_ERR_INVALID_ARG;
+    if (!aligned(pool, 16) || !aligned(block_table, 4) || !aligned(ends, 4) || !aligned(lens, 4))
+        return BQ_ERR_MISALIGNED;
+    p->pool = static_cast<uint8_t *>(const_cast<void *>(pool));
+    p->page_stride = page_stride;
+    p->block_bytes = block;
+    p->pages = static_cast<int>(pages);
+    p->kv_heads = static_cast<int>(kv_heads);
+    p->head_dim = static_cast<int>(head_dim);
+    p->group_size = static_cast<int>(group_size);
+    p->page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    p->table = block_table;
+    p->table_ld = table_ld;
+    p->table_width = static_cast<int>(table_width);
+    s->cu = ends;
+    s->lens = lens;
+    s->batch = static_cast<int>(batch);
+    s->uniform_n = ends == nullptr ? static_cast<int>(total / batch) : 0;
+    return BQ_OK;
+}
+
 inline bq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? BQ_OK : BQ_ERR_CUDA; }
 
 // Which kernels a BitLinear call of this shape runs (a bq_bitlinear_path).
@@ -746,6 +796,117 @@ bq_status bq_linear_w4_grouped(const float *x, int64_t M, int64_t K, const uint3
     if (st != BQ_OK) return st;
     return from_cuda(launch_linear_w4(x, M, K, qweight, scales_f16, qzeros, bias, N, group_size, out, workspace,
                                       static_cast<cudaStream_t>(stream), dev));
+}
+
+size_t bq_kv4_page_bytes(int64_t page_size, int64_t head_dim, int64_t group_size) {
+    if (!kv4_sizes_ok(page_size, head_dim, group_size)) return 0;
+    return static_cast<size_t>(page_size * (head_dim + 8 * (head_dim / group_size)));
+}
+
+bq_status bq_kv4_write(const void *k, const void *v, bq_dtype dtype, int64_t total, int64_t kv_heads,
+                       int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                       int64_t v_head_stride, const int32_t *cu_q, const int32_t *seq_lens, int64_t batch,
+                       const int32_t *block_table, int64_t table_ld, int64_t table_width, void *pool, int64_t pages,
+                       int64_t page_stride, int64_t page_size, int64_t group_size, bq_stream_t stream) {
+    if (!out_dtype_ok(dtype)) return BQ_ERR_INVALID_ARG;
+    Kv4WriteArgs a;
+    bool empty = false;
+    bq_status st = kv4_check(pool, pages, page_stride, page_size, kv_heads, head_dim, group_size, block_table,
+                             table_ld, table_width, cu_q, seq_lens, batch, total, &a.pool, &a.seqs, &empty);
+    if (st != BQ_OK || empty) return st;
+    if (k == nullptr || v == nullptr || seq_lens == nullptr || k_token_stride < 0 || k_head_stride < 0 ||
+        v_token_stride < 0 || v_head_stride < 0)
+        return BQ_ERR_INVALID_ARG;
+    const int64_t e = 16 / esize(dtype);
+    if (!aligned(k, 16) || !aligned(v, 16) || k_token_stride % e != 0 || k_head_stride % e != 0 ||
+        v_token_stride % e != 0 || v_head_stride % e != 0)
+        return BQ_ERR_MISALIGNED;
+    DevInfo dev;
+    st = current_device(&dev);
+    if (st != BQ_OK) return st;
+    a.k = k;
+    a.v = v;
+    a.dtype = dtype;
+    a.k_tok = k_token_stride;
+    a.k_head = k_head_stride;
+    a.v_tok = v_token_stride;
+    a.v_head = v_head_stride;
+    a.total = total;
+    return from_cuda(launch_kv4_write(a, static_cast<cudaStream_t>(stream), dev));
+}
+
+bq_status bq_kv4_read(const void *pool, int64_t pages, int64_t page_stride, int64_t page_size, int64_t kv_heads,
+                      int64_t head_dim, int64_t group_size, const int32_t *block_table, int64_t table_ld,
+                      int64_t table_width, const int32_t *starts, const int32_t *cu_len, int64_t batch, int64_t total,
+                      bq_dtype out_dtype, void *k, void *v, bq_stream_t stream) {
+    if (!out_dtype_ok(out_dtype)) return BQ_ERR_INVALID_ARG;
+    Kv4ReadArgs a;
+    bool empty = false;
+    if (cu_len == nullptr && total > 0 && batch > 0) return BQ_ERR_INVALID_ARG;
+    bq_status st = kv4_check(pool, pages, page_stride, page_size, kv_heads, head_dim, group_size, block_table,
+                             table_ld, table_width, cu_len, nullptr, batch, total, &a.pool, &a.seqs, &empty);
+    if (st != BQ_OK || empty) return st;
+    if (k == nullptr || v == nullptr) return BQ_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4)) return BQ_ERR_MISALIGNED;
+    DevInfo dev;
+    st = current_device(&dev);
+    if (st != BQ_OK) return st;
+    a.k = k;
+    a.v = v;
+    a.dtype = out_dtype;
+    a.total = total;
+    a.starts = starts;
+    return from_cuda(launch_kv4_read(a, static_cast<cudaStream_t>(stream), dev));
+}
+
+size_t bq_kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    if (total < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1) return 0;
+    return kv4_attention_workspace_bytes(total, q_heads, kv_heads, head_dim);
+}
+
+bq_status bq_kv4_attention(const void *q, bq_dtype dtype, int64_t total, int64_t q_heads, int64_t head_dim,
+                           int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_q, int64_t max_q,
+                           const int32_t *seq_lens, int64_t batch, const int32_t *block_table, int64_t table_ld,
+                           int64_t table_width, const void *pool, int64_t pages, int64_t page_stride,
+                           int64_t page_size, int64_t kv_heads, int64_t group_size, float scale, int64_t window,
+                           float softcap, const float *slopes, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, bq_stream_t stream) {
+    if (!out_dtype_ok(dtype) || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || !std::isfinite(scale) ||
+        !std::isfinite(softcap) || softcap < 0.0f || window < 0)
+        return BQ_ERR_INVALID_ARG;
+    if (dtype == BQ_F32 || q_heads > kMaxQHeads) return BQ_ERR_UNSUPPORTED;
+    Kv4AttnArgs a;
+    bool empty = false;
+    bq_status st = kv4_check(pool, pages, page_stride, page_size, kv_heads, head_dim, group_size, block_table,
+                             table_ld, table_width, cu_q, seq_lens, batch, total, &a.pool, &a.seqs, &empty);
+    if (st != BQ_OK || empty) return st;
+    if (q == nullptr || out == nullptr || seq_lens == nullptr || q_token_stride < 0 || q_head_stride < 0 ||
+        (cu_q != nullptr && max_q < 1))
+        return BQ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 != 0 || q_head_stride % 8 != 0 ||
+        !aligned(slopes, 4) || !aligned(lse, 4))
+        return BQ_ERR_MISALIGNED;
+    const size_t need = kv4_attention_workspace_bytes(total, q_heads, kv_heads, head_dim);
+    if (workspace == nullptr || workspace_bytes < need) return BQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return BQ_ERR_MISALIGNED;
+    DevInfo dev;
+    st = current_device(&dev);
+    if (st != BQ_OK) return st;
+    a.q = q;
+    a.dtype = dtype;
+    a.q_tok = q_token_stride;
+    a.q_head = q_head_stride;
+    a.total = total;
+    a.q_heads = static_cast<int>(q_heads);
+    a.max_q = cu_q == nullptr ? a.seqs.uniform_n : static_cast<int>(max_q < total ? max_q : total);
+    a.scale = scale;
+    a.softcap = softcap;
+    a.window = window > kMaxDim ? 0 : static_cast<int>(window);  // (no sequence is longer)
+    a.slopes = slopes;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    return from_cuda(launch_kv4_attention(a, static_cast<cudaStream_t>(stream), dev));
 }
 
 }  // extern "C"

@@ -24,6 +24,9 @@ enum Site : uint32_t {
     SITE_INT4_PACK = 16,
     SITE_W4_STAGE = 17,
     SITE_W4_DRAIN = 18,
+    SITE_KV4_WRITE = 32,
+    SITE_KV4_READ = 33,
+    SITE_KV4_ATTENTION = 34,
 };
 
 __device__ __forceinline__ void report(uint32_t *status, uint32_t code, uint32_t site) {

@@ -214,6 +214,63 @@ bq_status launch_bitlinear_backward(const void *x, bq_dtype xt, const void *dout
                                     const uint32_t *wpacked, const float *w_scale, int64_t N, float eps, float *dx,
                                     float *dw, void *workspace, cudaStream_t s, const DevInfo &dev);
 
+// 4-bit key/value cache (kv4_cache.cu, kv4_attention.cu).  A pool as the
+// kernels see it, with the pages of each sequence.
+struct Kv4Pool {
+    uint8_t *pool = nullptr;
+    int64_t page_stride = 0;      // bytes between pages
+    int64_t block_bytes = 0;      // bytes of one (page, head) block
+    int pages = 0, kv_heads = 0, head_dim = 0, group_size = 0;
+    int page_log2 = 0;
+    const int32_t *table = nullptr;  // [batch][table_ld] page numbers
+    int64_t table_ld = 0;
+    int table_width = 0;
+};
+// The sequences of a batch: rows cu[b] .. cu[b+1] (or uniform_n rows each, cu
+// nullptr), and the cached tokens of each after the call's rows were written.
+struct Kv4Seqs {
+    const int32_t *cu = nullptr;
+    const int32_t *lens = nullptr;
+    int batch = 0, uniform_n = 0;
+};
+constexpr int kKv4BlockTokens = 64;  // most tokens that one block of the write and the read takes
+struct Kv4WriteArgs {
+    const void *k = nullptr, *v = nullptr;
+    bq_dtype dtype = BQ_BF16;
+    int64_t k_tok = 0, k_head = 0, v_tok = 0, v_head = 0;  // strides in elements
+    int64_t total = 0;
+    Kv4Seqs seqs;
+    Kv4Pool pool;
+};
+cudaError_t launch_kv4_write(const Kv4WriteArgs &a, cudaStream_t s, const DevInfo &dev);
+struct Kv4ReadArgs {
+    void *k = nullptr, *v = nullptr;  // [total][kv_heads][head_dim]
+    bq_dtype dtype = BQ_BF16;
+    int64_t total = 0;
+    const int32_t *starts = nullptr;  // first position read of each sequence, or nullptr for 0
+    Kv4Seqs seqs;
+    Kv4Pool pool;
+};
+cudaError_t launch_kv4_read(const Kv4ReadArgs &a, cudaStream_t s, const DevInfo &dev);
+struct Kv4AttnArgs {
+    const void *q = nullptr;  // [total][q_heads][head_dim], strides in elements
+    bq_dtype dtype = BQ_BF16;
+    int64_t q_tok = 0, q_head = 0;
+    int64_t total = 0;
+    int q_heads = 0;
+    int max_q = 0;  // most rows of one sequence
+    float scale = 0.0f, softcap = 0.0f;
+    int window = 0;
+    const float *slopes = nullptr;
+    void *out = nullptr;  // [total][q_heads][head_dim]
+    float *lse = nullptr;  // [total][q_heads] or nullptr
+    void *workspace = nullptr;
+    Kv4Seqs seqs;
+    Kv4Pool pool;
+};
+size_t kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev);
+
 // Grouped INT4 linear.
 size_t linear_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t group_size);
 // Multi-token path on the tensor cores (2..32 tokens, K % 1024 == 0, groups of 128k).

@@ -2,7 +2,9 @@
  * bq.h - C ABI of libbq.so, a B200 (sm_100a) implementation of the quantized
  * linear layer: per-token int8 activation quantization after a
  * parameter-free RMSNorm, ternary (absmean) or grouped affine INT4 weights,
- * and integer matmuls with a fused dequantizing epilogue.
+ * and integer matmuls with a fused dequantizing epilogue; and of the 4-bit
+ * key/value cache that a model decoding with such layers keeps: quantized as
+ * it is written, read back, and attended to.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -42,6 +44,14 @@
  *    packed the same way along the group axis (G = K / group_size, ragged
  *    last word zero-padded); scales IEEE binary16 [N][G]; dequantized weight
  *    w[n,k] = scale[n,g] * (q[n,k] - zero[n,g]) with g = k / group_size.
+ *  - 4-bit key/value cache (bq_kv4_write, bq_kv4_read, bq_kv4_attention): a
+ *    pool of pages, each [kv_heads] blocks of bq_kv4_page_bytes() bytes.  The
+ *    block of one page and head holds page_size tokens: key codes
+ *    [page_size][D/2] bytes (element d in bits [4*(d%2), 4*(d%2)+3] of byte
+ *    d/2), key parameters [page_size][D/G] pairs of binary16 (step s, minimum
+ *    m), then value codes and value parameters in the same form.  A stored
+ *    element stands for s * code + m.  Position p of sequence b is token
+ *    p % page_size of page block_table[b][p / page_size].
  */
 #ifndef BQ_H
 #define BQ_H
@@ -466,6 +476,111 @@ bq_status bq_bitlinear_w2a8_noalloc(const void *x, bq_dtype x_dtype, int64_t M, 
                                     const uint32_t *wpacked, const float *w_scale, int64_t N,
                                     const float *bias, float eps, bq_dtype out_dtype, void *out,
                                     bq_stream_t stream);
+
+/*
+ * 4-bit key/value cache.
+ *
+ * Arguments shared by the three calls below:
+ *   pool, pages, page_stride: `pages` pages, page_stride bytes apart (a
+ *     multiple of 16, at least kv_heads * bq_kv4_page_bytes()); pool is
+ *     16-byte aligned.
+ *   head_dim D: 64 or 128.  group_size G: 64 or 128, at most D.  page_size:
+ *     16, 32, 64 or 128 tokens.  (Other sizes: BQ_ERR_UNSUPPORTED.)
+ *   block_table: int32 [batch][table_ld], the first table_width entries of a
+ *     row naming the pages of a sequence in order.  Only entries whose
+ *     positions the call reaches are read.  An entry outside [0, pages), or a
+ *     position behind the table, records BQ_ERR_INVALID_ARG in the device
+ *     status word; the call then skips (write) or gives NaN for (read,
+ *     attention) what it would have held, and touches no other memory.
+ *   cu_q: int32 [batch + 1], the rows of sequence b being cu_q[b] up to
+ *     cu_q[b+1] (cu_q[0] = 0, not decreasing, cu_q[batch] <= total); or NULL:
+ *     total / batch rows each (total must be a multiple of batch).  Rows
+ *     behind cu_q[batch] are neither read nor written.
+ *   seq_lens: int32 [batch], tokens of the sequence in the cache including
+ *     the call's rows, so that row j of n stands at position
+ *     seq_lens[b] - n + j.  A row whose position is negative has no place: it
+ *     is not written, and attends to nothing.
+ *   total, batch: rows in all and sequences; total == 0 or batch == 0 is a
+ *     valid empty call.
+ * Tables, lengths and offsets are read on the device: a captured call can be
+ * replayed with new ones.
+ */
+
+/* Bytes of one page and head: page_size * (D + 8 * D / G); 0 for sizes that
+ * are not supported. */
+size_t bq_kv4_page_bytes(int64_t page_size, int64_t head_dim, int64_t group_size);
+
+/*
+ * Quantizes new key and value rows into their pages.  For each group of G
+ * elements x of a row (of one token and head):
+ *
+ *   m = half(clamp(min x, -65504, 65504))
+ *   s = half(min(fl32(fl32(max x - m) / 15), 65504))
+ *   code = clamp(rne((x - m) / s), 0, 15), the quotient of the real numbers
+ *          (s = 0: code 0)
+ *
+ * A group whose range max x - min x is not finite in fp32 (an infinity or a
+ * NaN in it) is stored as NaN.
+ *
+ * k, v: [total][kv_heads][D] of dtype BQ_F32, BQ_BF16 or BQ_F16, unit inner
+ * stride, token and head strides in elements (multiples of 16 bytes), 16-byte
+ * aligned.  Two rows of one call with the same place in the pool (sequences
+ * that share a page they write) leave that place undefined.
+ */
+bq_status bq_kv4_write(const void *k, const void *v, bq_dtype dtype, int64_t total, int64_t kv_heads,
+                       int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                       int64_t v_head_stride, const int32_t *cu_q, const int32_t *seq_lens, int64_t batch,
+                       const int32_t *block_table, int64_t table_ld, int64_t table_width, void *pool, int64_t pages,
+                       int64_t page_stride, int64_t page_size, int64_t group_size, bq_stream_t stream);
+
+/*
+ * Reads positions starts[b] + j of each sequence (j < cu_len[b+1] - cu_len[b];
+ * starts int32 [batch], or NULL for 0) into rows cu_len[b] + j of k and v,
+ * both dense [total][kv_heads][D] of out_dtype, 16-byte aligned:
+ * out_dtype(fl32(s * code + m)).  cu_len: int32 [batch + 1] as cu_q above,
+ * not NULL.  A negative position gives NaN and sets the status word.
+ */
+bq_status bq_kv4_read(const void *pool, int64_t pages, int64_t page_stride, int64_t page_size, int64_t kv_heads,
+                      int64_t head_dim, int64_t group_size, const int32_t *block_table, int64_t table_ld,
+                      int64_t table_width, const int32_t *starts, const int32_t *cu_len, int64_t batch, int64_t total,
+                      bq_dtype out_dtype, void *k, void *v, bq_stream_t stream);
+
+/* Workspace of bq_kv4_attention for up to `total` rows. */
+size_t bq_kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * Causal attention of the batch's rows over the cache.  Row i of sequence b
+ * at position p = seq_lens[b] - n + j sees the positions t with t <= p and,
+ * where window > 0, t > p - window.  With key and value elements as stored:
+ *
+ *   z[t] = scale * sum_d q[d] * K[t,d];   softcap > 0: z = softcap * tanh(z / softcap)
+ *   slopes: z[t] += slopes[h] * (t - p)
+ *   out = sum_t softmax(z)[t] * V[t],   lse = log sum_t exp(z[t])
+ *
+ * A row that sees nothing gives 0 and lse = -inf.  A query row that holds a
+ * NaN or an infinity, or sees a token stored as NaN, gives NaN.  Tokens that
+ * a row does not see take no part, whatever their pages hold.
+ *
+ * q: [total][q_heads][D] of dtype BQ_BF16 or BQ_F16 (BQ_F32:
+ * BQ_ERR_UNSUPPORTED), unit inner stride, token and head strides in elements
+ * (multiples of 16 bytes), 16-byte aligned; q_heads a multiple of kv_heads,
+ * query head h reading key head h / (q_heads / kv_heads).  max_q: at least the
+ * rows of the longest sequence (rows behind it are left out); ignored where
+ * cu_q is NULL.  scale finite; softcap finite and >= 0 (0: none); window >= 0
+ * (0: none); slopes fp32 [q_heads] or NULL.  out: dense [total][q_heads][D] of
+ * dtype, 16-byte aligned.  lse: fp32 [total][q_heads] or NULL.
+ * workspace: at least bq_kv4_attention_workspace_bytes(total, ...) bytes,
+ * 256-byte aligned; it carries nothing from one call to the next, but two
+ * calls that run at the same time need one each.  The result does not depend
+ * on timing: the same call gives the same bits.
+ */
+bq_status bq_kv4_attention(const void *q, bq_dtype dtype, int64_t total, int64_t q_heads, int64_t head_dim,
+                           int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_q, int64_t max_q,
+                           const int32_t *seq_lens, int64_t batch, const int32_t *block_table, int64_t table_ld,
+                           int64_t table_width, const void *pool, int64_t pages, int64_t page_stride,
+                           int64_t page_size, int64_t kv_heads, int64_t group_size, float scale, int64_t window,
+                           float softcap, const float *slopes, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, bq_stream_t stream);
 
 /* Workspace bytes a call needs (0 for calls that need none). */
 size_t bq_workspace_bytes(bq_op op, int64_t M, int64_t N, int64_t K, int64_t group_size);
