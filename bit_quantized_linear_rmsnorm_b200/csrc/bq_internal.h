@@ -270,6 +270,8 @@ struct Kv4AttnArgs {
 };
 size_t kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev);
+cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev);
+constexpr int64_t kKv4FewColumns = 24;  // rows of a sequence * query heads of a key head up to which the cache bounds
 
 // Grouped INT4 linear.
 size_t linear_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t group_size);

@@ -39,7 +39,7 @@
 // BQ_ERR_TIMEOUT, lets its copies land (bounded again) and finishes.
 #include <algorithm>
 
-#include "kv4_common.cuh"
+#include "kv4_attention.cuh"
 
 namespace bq {
 namespace {
@@ -47,9 +47,6 @@ namespace {
 constexpr int kTile = 32;
 constexpr int kW = 8;  // warps
 constexpr int kThreads = kW * 32;
-constexpr int kMaxSms = 160;
-constexpr float kNoMax = -3.0e38f;  // running maximum before any token
-constexpr float kLift = 7.0f;       // weights at the maximum are 2^7
 constexpr float kSlack = 8.0f;      // a maximum is raised when passed by more
 constexpr float kFarStep = 0.001953125f;  // a step below 2^-9 of the largest is far from it
 
@@ -77,15 +74,6 @@ struct Shape {
     static constexpr size_t SLOT = static_cast<size_t>(COLS) * (D + 4);  // floats of a partial result
 };
 
-struct Partial {  // an item that begins in a CTA and ends in a later one
-    int b, head, cb, count;
-};
-
-struct Ws {
-    Partial *desc;
-    float *slots;
-};
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -98,48 +86,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-// {lo, hi} as a pair of fp16
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) { return pack_f16(lo, hi); }
-
 // What the rows of sequence b need of the cache.
 struct SeqPlan {
     int64_t first;  // first row
@@ -169,7 +115,7 @@ __device__ __forceinline__ SeqPlan plan_seq(const Kv4AttnArgs &a, int b, int sha
 }
 
 template <typename C, bool MODS, typename T>
-__global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4AttnArgs a, const Ws ws, uint32_t *status) {
+__global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4AttnArgs a, const Kv4Ws ws, uint32_t *status) {
     constexpr int D = C::D, NB = C::NB, HV = C::HV, GR = C::GR;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sum[kW];
@@ -757,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
         float *slot = ws.slots + (2 * cta + (u == item_begin ? 1 : 0)) * C::SLOT;
         if (!whole && u == item_begin && threadIdx.x == 0) {
             const int64_t last = (item_end * ctas - 1) / total;  // CTA that holds the item's last unit
-            ws.desc[cta] = {b, head, cb, static_cast<int>(last - cta) + 1};
+            ws.desc[cta] = {p.first, col0, ncols, head, static_cast<int>(last - cta) + 1};
         }
         for (int e = threadIdx.x; e < ncols * (D / 4); e += kThreads) {
             const int c = e / (D / 4), d = (e % (D / 4)) * 4;
@@ -811,74 +757,25 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
     }
 }
 
-// Joins the partial results of the items that span several CTAs.
-template <typename C, typename T>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Kv4AttnArgs a, const Ws ws) {
-    constexpr int D = C::D;
-    pdl_wait();
-    const int64_t cta = blockIdx.x;
-    const Partial it = ws.desc[cta];
-    if (it.count <= 1) return;
-    const int share = a.q_heads / a.pool.kv_heads;
-    const SeqPlan p = plan_seq(a, it.b, share, C::COLS);
-    const int e = blockIdx.y * kThreads + threadIdx.x;
-    const int c = e / D, d = e % D;
-    if (c >= min(C::COLS, p.rows * share - it.cb * C::COLS)) return;
-    const int64_t stride = static_cast<int64_t>(2 * C::SLOT);
-    const float *s0 = ws.slots + (2 * cta + 1) * C::SLOT + c * (D + 4);
-    const float *s1 = ws.slots + 2 * (cta + 1) * C::SLOT + c * (D + 4);  // then 2 slots on
-    float top = s0[D];
-#pragma unroll 8
-    for (int i = 1; i < it.count; ++i) top = fmaxf(top, s1[(i - 1) * stride + D]);
-    float k = ex2(s0[D] - top);
-    float num = s0[d] * k, den = s0[D + 2 + d / C::G] * k, sum = s0[D + 1] * k;
-#pragma unroll 8
-    for (int i = 1; i < it.count; ++i) {
-        const float *s = s1 + (i - 1) * stride;
-        k = ex2(s[D] - top);
-        num = fmaf(s[d], k, num);
-        den = fmaf(s[D + 2 + d / C::G], k, den);
-        sum = fmaf(s[D + 1], k, sum);
-    }
-    const int col = it.cb * C::COLS + c, row = col / share, hh = col - row * share;
-    const int64_t to = (p.first + row) * a.q_heads + static_cast<int64_t>(it.head) * share + hh;
-    const float v = den == 0.0f ? 0.0f : num * __fdividef(1.0f, den);
-    const uint32_t v2 = pack2(v, 0.0f, T());
-    reinterpret_cast<uint16_t *>(a.out)[to * D + d] = static_cast<uint16_t>(v2 & 0xffffu);
-    if (a.lse != nullptr && d == 0)
-        a.lse[to] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
-}
-
 template <typename C, bool MODS, typename T>
 cudaError_t launch_decode(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {
     auto kern = kv4_decode_kernel<C, MODS, T>;
     static SmemOptIn opt_in;
     cudaError_t e = smem_opt_in(opt_in, dev, reinterpret_cast<const void *>(kern), static_cast<size_t>(C::SMEM));
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(std::min(dev.num_sms, kMaxSms) * C::CTAS);
-    Ws ws;
-    ws.desc = static_cast<Partial *>(a.workspace);
-    ws.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + 2 * kMaxSms * sizeof(Partial));
+    const unsigned grid = static_cast<unsigned>(std::min(dev.num_sms, kKv4MaxSms) * C::CTAS);
+    const Kv4Ws ws = kv4_workspace(a.workspace);
     kern<<<grid, kThreads, C::SMEM, s>>>(a, ws, dev.status);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, C::COLS * C::D / kThreads);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<C, T>, a, ws);
+    return e != cudaSuccess ? e : kv4_launch_join<C::D, C::G, C::COLS, T>(a, ws, grid, s);
 }
 
 }  // namespace
 
-size_t kv4_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t head_dim) {
-    // one CTA per SM with 24 columns, or two with 8: 2 slots each
-    return 2 * kMaxSms * (sizeof(Partial) + 24 * static_cast<size_t>(head_dim + 4) * 4);
+size_t kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    // slots of a CTA: 2, for one CTA per SM with 24 columns, or two with 8; many rows: one with 256
+    const int64_t cols = total * (q_heads / kv_heads) > kKv4FewColumns ? 256 : 24;
+    return 2 * kKv4MaxSms * (sizeof(Kv4Partial) + static_cast<size_t>(cols * (head_dim + 4)) * 4);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {
@@ -891,6 +788,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t s, const Dev
             using C = decltype(c);
             return mods ? launch_decode<C, true, T>(a, s, dev) : launch_decode<C, false, T>(a, s, dev);
         };
+        if (cols > kKv4FewColumns) return launch_kv4_prefill(a, s, dev);
         if (cols <= 8) return go(Shape<D, G, 1>());
         if (cols <= 16) return go(Shape<D, G, 2>());
         return go(Shape<D, G, 3>());

@@ -1,0 +1,984 @@
+// Attention of many query rows over the 4-bit key/value cache (prompts, and
+// chunks of them): bound by the tensor cores, and by the exponentials.
+//
+// Arithmetic.  As with few rows (kv4_attention.cu) the steps and minima stay
+// outside the products, whose operands are exact:
+//
+//   S = Q C_k^T         Q: rows scaled by powers of two into fp16, C_k: key codes
+//   z = f (S s_k + q' m_k)           f, q' = sum(q) per row, s_k, m_k per token
+//   w = fp16(2^(z - M + 7) mu)       value step s_v = mu 2^e, 1 <= mu < 2
+//   [O | L] += w [c_v 2^(e - e0) | 1/mu | m_v/mu 2^-e1]
+//
+// so that the output is (2^e0 O + 2^e1 L_m) / L_1: the divisor and the minima's
+// term are sums of the same rounded weights w as the codes' term, and the
+// rounding of a weight (2^-11 at most) changes how much a token counts, never
+// what it stands for.  1/mu and m_v/mu are pairs of fp16 (22 bits).  The
+// exponents e0, e1 follow the largest step and minimum so far (with room, so
+// that they hardly ever move; the sums are rescaled if they do).  A code of a
+// key is an fp16 subnormal masked out of its word (c 2^-24 or, the word's
+// upper half of a byte, 16 c 2^-24: Q takes the 16), of a value an fp16
+// 1024 + c brought to c 2^k by one fused multiply-add; both are exact.
+//
+// Roles of the 512 threads of a CTA (one per SM), which takes 256 columns
+// (pairs of query row and head of one key head) as two tiles of 128:
+//   warps 0-3, 4-7   softmax of a tile, a thread per row: S from TMEM, w back
+//                    to TMEM in the place of S, as the next product's A operand
+//   warps 8-10       values: one (token, group) per thread from 4 bits to fp16
+//   warps 11-13      the same for keys
+//   warp 14          issues the products (tcgen05.mma kind::f16)
+//   warp 15          copies pages (bulk copies of K and V codes and parameters)
+// A tile of tokens is unpacked once for both tiles of rows, and the products
+// of one tile run while the other's softmax does.
+//
+// Work.  The (sequence, head, 256 columns) items of the batch are one list
+// whose cost (about the tokens that an item reads) has a closed form; the CTAs
+// take equal shares of it, cutting items where a share ends, and the joining
+// kernel adds up what was cut.
+//
+// Every wait is bounded; if one runs out the kernel records BQ_ERR_TIMEOUT,
+// lets its copies and products end (bounded again) and finishes.
+#include <algorithm>
+
+#include "kv4_attention.cuh"
+
+namespace bq {
+namespace {
+
+constexpr int kRows = 128;     // of a tile
+constexpr int kCols = 256;     // columns of an item
+constexpr int kPThreads = 512;
+constexpr int kRing = 3;       // raw stages
+constexpr float kRise = 7.0f;  // the running maximum is raised when passed by more
+constexpr int kOverhead = 192; // cost of starting an item, in tokens
+
+template <int D_, int G_>
+struct PShape {
+    static constexpr int D = D_, G = G_, GR = D / G;
+    static constexpr int TOK = GR == 1 ? 96 : 48;  // tokens of a tile: 96 threads unpack (token, group) pairs
+    static constexpr int ROW = D / 2, PAR = 4 * GR;
+    static constexpr int RAW = TOK * 2 * (ROW + PAR);
+    static constexpr int OC = D + 16 * GR;         // columns of [O | L]
+    static constexpr int QB = kRows * D * 2;       // bytes of a tile of Q
+    static constexpr int KB = TOK * D * 2;
+    static constexpr int VB = TOK * OC * 2;
+    static constexpr int PB = TOK * GR * 3 * 4;    // s_k, m_k, mu
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + 2 * QB;
+    static constexpr int OFF_V = OFF_K + 2 * KB;
+    static constexpr int OFF_RAW = OFF_V + 2 * VB;
+    static constexpr int OFF_P = OFF_RAW + kRing * RAW;
+    static constexpr int SMEM = OFF_P + 2 * PB;
+    static_assert(SMEM <= 231000, "shared memory of a CTA");
+    // TMEM columns: S (and w in its place), then [O | L], of each tile
+    static constexpr int SC = 96;
+    static constexpr int T_O = 2 * SC;
+    static_assert(T_O + 2 * OC <= 512, "TMEM");
+};
+
+// What a tile of tokens tells the softmax beside its parameters.
+struct TileInfo {
+    int e0, e1;
+    int odd;  // holds values that are not finite
+};
+
+__device__ __forceinline__ uint64_t pack64(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack64(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float pow2i(int e) {  // 2^e, 0 below 2^-126
+    return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23);
+}
+__device__ __forceinline__ int exp_of(float x) {  // of a finite x; 2^-24 and less give -24
+    return max(static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127, -24);
+}
+__device__ __forceinline__ void lds128(uint32_t a, uint64_t &x, uint64_t &y) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts32f(uint32_t a, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+
+// ---- tensor cores
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Operand without a swizzle: blocks of 8 x 16 bytes, contiguous.  `lbo`: bytes
+// to the next block along K, `sbo`: along M or N (the same for both majors).
+__device__ __forceinline__ uint64_t desc_plain(uint32_t a, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((a >> 4) & 0x3fffu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+           (static_cast<uint64_t>(sbo >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+__host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {  // M = 128, fp16 x fp16 -> fp32
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t *r) {
+    static_assert(N == 32 || N == 16, "");
+    if constexpr (N == 32)
+        tmem_ld_32x32b_x32(a, *reinterpret_cast<uint32_t(*)[32]>(r));
+    else
+        tmem_ld_32x32b_x16(a, *reinterpret_cast<uint32_t(*)[16]>(r));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- the list of work
+// Cost of the items (blocks of kCols columns) of one head of a sequence:
+// kOverhead plus the tokens up to a block's last row, at least 1, at most what
+// the window leaves: an arithmetic sequence with flat ends.
+struct SeqWork {
+    int64_t first;  // first row
+    int64_t a0, step, cmax;
+    int64_t blocks;
+    int64_t cost;  // of one head
+    int rows, pos0, cap;
+};
+__device__ __forceinline__ int64_t cost_upto(const SeqWork &w, int64_t n) {
+    auto ceil_div = [](int64_t x, int64_t y) { return x <= 0 ? int64_t(0) : (x + y - 1) / y; };
+    const int64_t i1 = min(ceil_div(1 - w.a0, w.step), n);
+    const int64_t i2 = w.a0 > w.cmax ? i1 : max(i1, min((w.cmax - w.a0) / w.step + 1, n));
+    return n * kOverhead + i1 + (i2 - i1) * w.a0 + w.step * ((i1 + i2 - 1) * (i2 - i1) / 2) + (n - i2) * w.cmax;
+}
+__device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int share) {
+    SeqWork w;
+    int n;
+    kv4_rows(a.seqs, b, w.first, n);
+    w.rows = static_cast<int>(min(static_cast<int64_t>(min(n, a.max_q)), a.total - w.first));
+    if (n <= 0 || w.rows < 0 || w.first < 0) w.rows = 0;
+    w.pos0 = static_cast<int>(max(static_cast<int64_t>(__ldg(a.seqs.lens + b)) - n, int64_t(-0x7fffffff)));
+    w.cap = static_cast<int>(min(static_cast<int64_t>(a.pool.table_width) << a.pool.page_log2, int64_t(0x7fffffff)));
+    w.step = max(kCols / share, 1);
+    w.a0 = w.pos0 + w.step;
+    w.cmax = a.window > 0 ? a.window + w.step : int64_t(1) << 40;
+    w.blocks = (static_cast<int64_t>(w.rows) * share + kCols - 1) / kCols;
+    w.cost = cost_upto(w, w.blocks);
+    return w;
+}
+
+// The parts of items that make up a CTA's share, one after the other; every
+// role walks them by itself.
+struct Segment {
+    int b, head, col0, ncols;
+    int start, hi;     // first token of the first tile, last token that is read (-1: none)
+    int tile0, tiles;  // tiles of this part
+    int pos0, cap;
+    int64_t first;
+    bool begins, whole;
+    int64_t end;       // of the item, in the list
+};
+struct Walk {
+    int64_t at, stop, seq_begin;
+    int b;
+};
+template <int TOK, int ALIGN>
+__device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, Walk &w, Segment &s) {
+    if (w.at >= w.stop) return false;
+    SeqWork q = seq_work(a, w.b, share);
+    while (w.at >= w.seq_begin + q.cost * a.pool.kv_heads) {
+        w.seq_begin += q.cost * a.pool.kv_heads;
+        q = seq_work(a, ++w.b, share);
+    }
+    const int64_t off = w.at - w.seq_begin;
+    const int64_t head = off / q.cost, rem = off - head * q.cost;
+    int64_t lo = 0, hi = q.blocks - 1;  // the last block whose cost begins at or below rem
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (cost_upto(q, mid) <= rem)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int64_t begin = w.seq_begin + head * q.cost + cost_upto(q, lo);
+    s.end = w.seq_begin + head * q.cost + cost_upto(q, lo + 1);
+    s.b = w.b;
+    s.head = static_cast<int>(head);
+    s.col0 = static_cast<int>(lo) * kCols;
+    s.ncols = static_cast<int>(min(int64_t(kCols), static_cast<int64_t>(q.rows) * share - s.col0));
+    s.first = q.first;
+    s.pos0 = q.pos0;
+    s.cap = q.cap;
+    const int r0 = s.col0 / share, r1 = (s.col0 + s.ncols - 1) / share;
+    const int64_t from = a.window > 0 ? max(static_cast<int64_t>(q.pos0) + r0 - a.window + 1, int64_t(0)) : 0;
+    s.start = static_cast<int>(from) & ~(ALIGN - 1);
+    s.hi = static_cast<int>(min(static_cast<int64_t>(q.pos0) + r1, static_cast<int64_t>(q.cap) - 1));
+    int tiles = 1;
+    if (s.hi < static_cast<int>(from)) {
+        s.hi = -1;  // nothing is seen, by any row
+        s.start = 0;
+    } else {
+        tiles = (s.hi - s.start) / TOK + 1;
+    }
+    const int64_t stop = min(s.end, w.stop), cost = s.end - begin;
+    s.tile0 = static_cast<int>((w.at - begin) * tiles / cost);
+    s.tiles = static_cast<int>(stop == s.end ? tiles : (stop - begin) * tiles / cost) - s.tile0;
+    s.begins = w.at == begin;
+    s.whole = s.begins && stop == s.end;
+    w.at = stop;
+    return true;
+}
+
+enum Bar {
+    RAW_FULL = 0,
+    RAW_EMPTY = RAW_FULL + kRing,
+    KV_FULL = RAW_EMPTY + kRing,
+    KV_EMPTY = KV_FULL + 2,
+    S_FULL = KV_EMPTY + 2,
+    P_FULL = S_FULL + 2,
+    Q_FULL = P_FULL + 2,
+    O_FULL = Q_FULL + 2,
+    DRAIN = O_FULL + 2,
+    kBars = DRAIN + 1
+};
+
+template <typename C, bool MODS, typename T>
+__global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4AttnArgs a, const Kv4Ws ws, uint32_t *status) {
+    constexpr int D = C::D, GR = C::GR, G = C::G, TOK = C::TOK, SC = C::SC, OC = C::OC;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t s_bars[kBars];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ TileInfo s_info[2];
+    __shared__ uint32_t s_bad[kRing];
+    __shared__ int64_t s_sum[kPThreads / 32];
+    __shared__ int64_t s_before;
+    __shared__ int s_b;
+    pdl_launch_dependents();  // the joining kernel waits for this grid before it reads
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(smem), bars = smem_u32(s_bars);
+    const int share = a.q_heads / a.pool.kv_heads, H = a.pool.kv_heads, page_log2 = a.pool.page_log2;
+    auto bar = [&](int i) { return bars + 8 * i; };
+
+    // ---- this CTA's share
+    const int64_t per = (a.seqs.batch + kPThreads - 1) / kPThreads;
+    const int64_t b_lo = min(per * threadIdx.x, static_cast<int64_t>(a.seqs.batch));
+    const int64_t b_hi = min(b_lo + per, static_cast<int64_t>(a.seqs.batch));
+    int64_t mine = 0;
+    for (int64_t b = b_lo; b < b_hi; ++b) mine += seq_work(a, static_cast<int>(b), share).cost * H;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        ws.desc[blockIdx.x].count = 0;
+    }
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+    for (int w = 0; w < kPThreads / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + 2 * kOverhead - 1) / (2 * kOverhead));
+    const int64_t cta = blockIdx.x;
+    if (cta >= ctas) return;
+    Walk walk;
+    walk.at = total * cta / ctas;
+    walk.stop = total * (cta + 1) / ctas;
+    if (walk.at >= before && walk.at < before + mine) {
+        int64_t at = before;
+        for (int64_t b = b_lo; b < b_hi; ++b) {
+            const int64_t n = seq_work(a, static_cast<int>(b), share).cost * H;
+            if (walk.at < at + n) {
+                s_b = static_cast<int>(b);
+                s_before = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    if (warp == 14) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i)
+            mbar_init(bar(i), i >= RAW_EMPTY && i < KV_FULL ? 6
+                              : i >= KV_FULL && i < KV_EMPTY ? 6
+                              : (i >= P_FULL && i < O_FULL) ? 4 : 1);
+        fence_mbarrier_init();
+    }
+    // the columns of [O | L] behind the sums stay zero
+    for (int i = threadIdx.x; i < 2 * GR * TOK; i += kPThreads) {
+        const int buf = i / (GR * TOK), r = i / TOK % GR, tok = i % TOK;
+        sts128(base + C::OFF_V + buf * C::VB + (r * (G / 8 + 2) + G / 8 + 1) * (TOK * 16) + tok * 16, 0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    walk.b = s_b;
+    walk.seq_begin = s_before;
+    const uint32_t tmem = s_tmem;
+    volatile int *abort = &s_abort;
+    Segment g;
+    // tiles start at a multiple of what one copy takes
+    const bool small_pages = page_log2 == 4;
+    auto next = [&]() {
+        return GR == 2 || small_pages ? next_segment<TOK, 16>(a, share, walk, g) : next_segment<TOK, 32>(a, share, walk, g);
+    };
+
+    if (warp < 8) {
+        regs_inc<184>();
+        // =================================================================== softmax
+        const int tile = warp >> 2, wl = warp & 3, row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
+        const uint32_t ts = tmem + tile * SC + lanes, to = tmem + C::T_O + tile * OC + lanes;
+        uint32_t n = 0;        // tiles so far, of all items (buffers)
+        uint32_t mine_n = 0;   // tiles so far of this tile of rows
+        uint32_t segs = 0;
+        bool ok = true;
+        while (ok && next()) {
+            if (g.tiles <= 0) {
+                // a share that ends before the first tile of what it holds: nothing to add
+                float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4));
+                const int c = tile * kRows + row;
+                slot[c * (D + 4) + D] = kNoMax;
+                slot[c * (D + 4) + D + 1] = 0.0f;
+            }
+            if (g.begins && !g.whole && threadIdx.x == 0) {
+                const int64_t last = (g.end * ctas - 1) / total;  // CTA that holds the item's end
+                ws.desc[cta] = {g.first, g.col0, g.ncols, g.head, static_cast<int>(last - cta) + 1};
+            }
+            if (g.tiles <= 0) continue;
+            if (tile * kRows >= g.ncols) {  // no rows for this tile
+                n += g.tiles;
+                continue;
+            }
+            const int c = tile * kRows + row;
+            const bool on = c < g.ncols;
+            const int qrow = (g.col0 + c) / share, hh = (g.col0 + c) - qrow * share;
+            const int pos = on ? g.pos0 + qrow : -1;
+            bool finite = true;
+            float f, sq[GR], slope2 = 0.0f;
+            {
+                const T *q = static_cast<const T *>(a.q) + (g.first + qrow) * a.q_tok +
+                             (static_cast<int64_t>(g.head) * share + hh) * a.q_head;
+                float top = 0.0f;
+                uint4 raw[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    raw[i] = make_uint4(0, 0, 0, 0);
+                    if (on) raw[i] = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    float x[8];
+                    Kv4In<T>::unpack(*reinterpret_cast<const uint4(*)[1]>(&raw[i]), x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        top = fmaxf(top, fabsf(x[j]));
+                        finite &= fabsf(x[j]) <= 3.402823466e38f;
+                    }
+                }
+                // 2^k brings the row's largest into [2^14, 2^15); a negative scale turns the row
+                int k = top > 0.0f && finite ? 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127) : 0;
+                k = min(k, 120);
+                const float up = !finite ? 0.0f : copysignf(__uint_as_float(static_cast<uint32_t>(127 + k) << 23), a.scale);
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+                const bool capped = MODS && a.softcap > 0.0f;
+                f = fabsf(a.scale) * 1.4426950408889634f * down * 16777216.0f;  // codes are c 2^-24
+                if (capped) f *= 2.0f / a.softcap;  // the argument of tanh, times 2 log2(e)
+                const uint32_t dst = base + C::OFF_Q + tile * C::QB + row * 16;
+#pragma unroll
+                for (int r = 0; r < GR; ++r) sq[r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    float x[8];
+                    Kv4In<T>::unpack(*reinterpret_cast<const uint4(*)[1]>(&raw[i]), x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        x[j] = finite ? x[j] * up : 0.0f;
+                        sq[i / (G / 8)] += x[j];
+                    }
+                    sts128(dst + i * (kRows * 16), pack_f16(x[0], x[4]), pack_f16(x[1] * 0.0625f, x[5] * 0.0625f),
+                           pack_f16(x[2], x[6]), pack_f16(x[3] * 0.0625f, x[7] * 0.0625f));
+                }
+#pragma unroll
+                for (int r = 0; r < GR; ++r) sq[r] *= 5.9604644775390625e-08f;  // 2^-24, as f has 2^24
+                if (MODS && a.slopes != nullptr && on)
+                    slope2 = __ldg(a.slopes + g.head * share + hh) * 1.4426950408889634f;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Q_FULL + tile));
+
+            const int row_lo = (g.col0 + tile * kRows) / share;
+            const int row_hi = (g.col0 + min(g.ncols, (tile + 1) * kRows) - 1) / share;
+            const int all_hi = min(g.pos0 + row_lo, g.hi);  // positions that every row of the tile sees
+            const int all_lo = a.window > 0 ? g.pos0 + row_hi - a.window + 1 : 0;
+            const int64_t see_lo = a.window > 0 ? static_cast<int64_t>(pos) - a.window + 1 : 0;
+
+            float m = kNoMax, sum = 0.0f;  // sum: of the weights, kept where it is asked for
+            int e0 = 0, e1 = 0;
+            for (int j = 0; j < g.tiles; ++j) {
+                const int tok0 = g.start + (g.tile0 + j) * TOK;
+                const int buf = n & 1;
+                // (S first: these threads may have left tiles out that are not theirs, and S tells that KV_FULL is at n)
+                ok = mbar_wait(bar(S_FULL + tile), mine_n & 1, abort, status, SITE_KV4_ATTENTION);
+                ok = ok && mbar_wait(bar(KV_FULL + buf), (n >> 1) & 1, abort, status, SITE_KV4_ATTENTION);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const TileInfo info = s_info[buf];
+                const bool edge = tok0 + TOK - 1 > all_hi || tok0 < all_lo || info.odd != 0;
+                const uint32_t par = base + C::OFF_P + buf * C::PB;
+                uint64_t y[TOK / 2];  // pairs of tokens
+                if constexpr (GR == 1) {
+#pragma unroll
+                    for (int i = 0; i < TOK; i += 32) tmem_ld<32>(ts + i, reinterpret_cast<uint32_t *>(y) + i);
+                    tmem_wait_ld();
+                    const uint64_t sq2 = pack64(sq[0], sq[0]);
+#pragma unroll
+                    for (int i = 0; i < TOK / 4; ++i) {
+                        uint64_t s0, s1, m0, m1;
+                        lds128(par + 16 * i, s0, s1);
+                        lds128(par + TOK * 4 + 16 * i, m0, m1);
+                        y[2 * i] = fma2(y[2 * i], s0, mul2(m0, sq2));
+                        y[2 * i + 1] = fma2(y[2 * i + 1], s1, mul2(m1, sq2));
+                    }
+                } else {
+                    const uint64_t sq2 = pack64(sq[0], sq[0]), sr2 = pack64(sq[1], sq[1]);
+#pragma unroll
+                    for (int h = 0; h < TOK; h += 16) {
+                        uint64_t u[8];
+                        tmem_ld<16>(ts + h, reinterpret_cast<uint32_t *>(y) + h);
+                        tmem_ld<16>(ts + TOK + h, reinterpret_cast<uint32_t *>(u));
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = h / 4; i < h / 4 + 4; ++i) {
+                            uint64_t s0, s1, m0, m1, t0, t1, n0, n1;
+                            lds128(par + 16 * i, s0, s1);
+                            lds128(par + TOK * 4 + 16 * i, t0, t1);
+                            lds128(par + TOK * 8 + 16 * i, m0, m1);
+                            lds128(par + TOK * 12 + 16 * i, n0, n1);
+                            y[2 * i] = fma2(y[2 * i], s0, fma2(u[2 * i - h / 2], t0, fma2(n0, sr2, mul2(m0, sq2))));
+                            y[2 * i + 1] =
+                                fma2(y[2 * i + 1], s1, fma2(u[2 * i + 1 - h / 2], t1, fma2(n1, sr2, mul2(m1, sq2))));
+                        }
+                    }
+                }
+                const uint32_t mu = par + 2 * GR * TOK * 4;
+
+                if constexpr (MODS) {  // scores in powers of two from here on
+                    const uint64_t f2 = pack64(f, f);
+                    const float cap2 = a.softcap * 1.4426950408889634f;
+                    const float away = static_cast<float>(tok0 - pos);
+#pragma unroll
+                    for (int i = 0; i < TOK / 2; ++i) {
+                        float2 z = unpack64(mul2(y[i], f2));
+                        if (a.softcap > 0.0f) {  // cap tanh(x) = cap (1 - 2 / (exp(2 x) + 1))
+                            z.x = fmaf(-2.0f * cap2, rcp(ex2(z.x) + 1.0f), cap2);
+                            z.y = fmaf(-2.0f * cap2, rcp(ex2(z.y) + 1.0f), cap2);
+                        }
+                        z.x = fmaf(slope2, away + static_cast<float>(2 * i), z.x);
+                        z.y = fmaf(slope2, away + static_cast<float>(2 * i + 1), z.y);
+                        y[i] = pack64(z.x, z.y);
+                    }
+                }
+                uint32_t seen[(TOK + 31) / 32];
+                if (edge) {
+#pragma unroll
+                    for (int w = 0; w < (TOK + 31) / 32; ++w) {
+                        const int64_t lo = max(see_lo - tok0 - 32 * w, int64_t(0));
+                        const int64_t hi = min(static_cast<int64_t>(min(pos, g.hi)) - tok0 - 32 * w, int64_t(31));
+                        seen[w] = hi < lo ? 0u : (0xffffffffu >> (31 - static_cast<int>(hi))) & (0xffffffffu << static_cast<int>(lo));
+                    }
+#pragma unroll
+                    for (int i = 0; i < TOK / 2; ++i) {
+                        const float2 z = unpack64(y[i]);
+                        y[i] = pack64((seen[i / 16] >> (2 * i % 32)) & 1u ? z.x : kNoMax,
+                                      (seen[i / 16] >> (2 * i % 32 + 1)) & 1u ? z.y : kNoMax);
+                    }
+                }
+                float top = kNoMax;
+#pragma unroll
+                for (int i = 0; i < TOK / 2; ++i) {
+                    const float2 z = unpack64(y[i]);
+                    top = fmaxf(top, fmaxf(z.x, z.y));
+                }
+                if (!MODS) top = fmaxf(top * f, kNoMax);
+
+                const bool rise = top > m + kRise;
+                if (__any_sync(0xffffffffu, rise) || (j > 0 && (info.e0 != e0 || info.e1 != e1))) {
+                    const float now = fmaxf(m, top), keep = ex2(m - now);
+                    m = now;
+                    sum *= keep;
+                    if (j > 0) {  // (the products up to here are complete: S came after them)
+                        const float ko = keep * pow2i(e0 - info.e0), km = keep * pow2i(e1 - info.e1);
+#pragma unroll
+                        for (int i = 0; i < OC; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld<16>(to + i, o);
+                            tmem_wait_ld();
+                            const bool sums = i % (G + 16) == G;
+#pragma unroll
+                            for (int t = 0; t < 16; ++t) {
+                                const float by = sums ? (t < 2 ? keep : km) : ko;
+                                o[t] = __float_as_uint(__uint_as_float(o[t]) * by);
+                            }
+                            tmem_st16(to + i, o);
+                        }
+                    }
+                }
+                e0 = info.e0;
+                e1 = info.e1;
+
+                const uint64_t f2 = MODS ? pack64(1.0f, 1.0f) : pack64(f, f);
+                const uint64_t off2 = pack64(kLift - m, kLift - m);
+#pragma unroll
+                for (int i = 0; i < TOK / 2; ++i) {
+                    const float2 x = unpack64(fma2(y[i], f2, off2));
+                    y[i] = pack64(ex2(x.x), ex2(x.y));
+                }
+                if (a.lse != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < TOK / 2; ++i) {
+                        const uint32_t bits = edge ? seen[i / 16] >> (2 * i % 32) : 3u;
+                        const float2 x = unpack64(y[i]);
+                        sum += (bits & 1u ? x.x : 0.0f) + (bits & 2u ? x.y : 0.0f);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < GR; ++r) {
+#pragma unroll
+                    for (int h = 0; h < TOK; h += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint64_t m0, m1;
+                            lds128(mu + (r * TOK + h + 4 * i) * 4, m0, m1);
+                            float2 x0 = unpack64(mul2(y[h / 2 + 2 * i], m0)), x1 = unpack64(mul2(y[h / 2 + 2 * i + 1], m1));
+                            if (edge) {
+                                const uint32_t bits = seen[h / 32] >> (h % 32 + 4 * i);
+                                x0.x = bits & 1u ? x0.x : 0.0f;
+                                x0.y = bits & 2u ? x0.y : 0.0f;
+                                x1.x = bits & 4u ? x1.x : 0.0f;
+                                x1.y = bits & 8u ? x1.y : 0.0f;
+                            }
+                            w[2 * i] = pack_f16(x0.x, x0.y);
+                            w[2 * i + 1] = pack_f16(x1.x, x1.y);
+                        }
+                        tmem_st8(ts + r * (TOK / 2) + h / 2, w);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(P_FULL + tile));
+                ++n;
+                ++mine_n;
+            }
+            if (!ok) break;
+            ok = mbar_wait(bar(O_FULL + tile), segs & 1, abort, status, SITE_KV4_ATTENTION);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            ++segs;
+            tc_fence_after();
+            // ---- results
+            const float w0 = pow2i(e0), w1 = pow2i(e1);
+            const bool spoilt = pos >= 0 && (!finite || pos >= g.cap);
+            if (pos >= g.cap) report(status, BQ_ERR_INVALID_ARG, SITE_KV4_ATTENTION);
+            const int64_t row_out = (g.first + qrow) * a.q_heads + static_cast<int64_t>(g.head) * share + hh;
+            float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4)) + c * (D + 4);
+#pragma unroll
+            for (int r = 0; r < GR; ++r) {
+                uint32_t l[16];
+                tmem_ld<16>(to + r * (G + 16) + G, l);
+                tmem_wait_ld();
+                float den = __uint_as_float(l[0]) + __uint_as_float(l[1]);
+                const float lm = (__uint_as_float(l[2]) + __uint_as_float(l[3])) * w1;
+                if (a.lse == nullptr && r == 0) sum = den;
+                if (spoilt) den = sum = __int_as_float(0x7fffffff);
+                const float inv = !g.whole ? 1.0f : den == 0.0f ? 0.0f : __fdividef(1.0f, den);
+#pragma unroll
+                for (int h = 0; h < G; h += 16) {
+                    uint32_t o[16];
+                    tmem_ld<16>(to + r * (G + 16) + h, o);
+                    tmem_wait_ld();
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {  // columns 0..7 of a block are dims 0 4 1 5 2 6 3 7
+                        const int d = (i & 8) + ((i & 1) << 2) + ((i & 7) >> 1);
+                        v[d] = fmaf(__uint_as_float(o[i]), w0, lm) * inv;
+                    }
+                    if (on) {
+                        if (g.whole) {
+                            uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row_out * D + r * G + h);
+                            out[0] = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
+                                                pack2(v[6], v[7], T()));
+                            out[1] = make_uint4(pack2(v[8], v[9], T()), pack2(v[10], v[11], T()), pack2(v[12], v[13], T()),
+                                                pack2(v[14], v[15], T()));
+                        } else {
+                            float4 *out = reinterpret_cast<float4 *>(slot + r * G + h);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                out[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                    }
+                }
+                if (on && !g.whole) {
+                    if (r == 0) {
+                        slot[D] = m;
+                        slot[D + 1] = sum;
+                    }
+                    slot[D + 2 + r] = den;
+                }
+                if (on && g.whole && r == 0 && a.lse != nullptr)
+                    a.lse[row_out] = sum == 0.0f ? -INFINITY : (m - kLift + log2f(sum)) * 0.6931471805599453f;
+            }
+            tc_fence_before();
+        }
+    } else {
+        regs_dec<72>();
+        if (warp < 14) {
+            // =============================================================== unpacking
+            const bool values = warp < 11;
+            const int u = (static_cast<int>(threadIdx.x) - (values ? 256 : 352));
+            const int tok = u % TOK, r = u / TOK;  // token and group of this thread
+            uint32_t n = 0;
+            int e0 = 0, e1 = 0;
+            bool ok = true;
+            while (ok && next()) {
+                if (g.tiles <= 0) continue;
+                const int align = GR == 2 || small_pages ? 16 : 32;
+                for (int j = 0; j < g.tiles; ++j, ++n) {
+                    const int stage = n % kRing, buf = n & 1;
+                    const int tok0 = g.start + (g.tile0 + j) * TOK;
+                    ok = n < 2 || mbar_wait(bar(KV_EMPTY + buf), ((n >> 1) - 1) & 1, abort, status, SITE_KV4_ATTENTION);
+                    ok = ok && mbar_wait(bar(RAW_FULL + stage), (n / kRing) & 1, abort, status, SITE_KV4_ATTENTION);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t raw = base + C::OFF_RAW + stage * C::RAW + (values ? TOK * (C::ROW + C::PAR) : 0);
+                    const uint32_t par = base + C::OFF_P + buf * C::PB;
+                    const bool held = tok0 + tok <= g.hi;
+                    const bool gone = (s_bad[stage] >> (tok / align)) & 1u;
+                    const uint32_t src = raw + tok * C::ROW + r * (G / 2);
+                    if (!values) {
+                        float2 x = unpack_f16(lds32(raw + TOK * C::ROW + tok * C::PAR + 4 * r));
+                        if (!held) x = make_float2(0.0f, 0.0f);
+                        if (gone) x.x = __int_as_float(0x7fffffff);
+                        sts32f(par + (r * TOK + tok) * 4, x.x);
+                        sts32f(par + ((GR + r) * TOK + tok) * 4, x.y);
+                        const uint32_t dst = base + C::OFF_K + buf * C::KB + r * (G / 8) * (TOK * 16) + tok * 16;
+#pragma unroll
+                        for (int i = 0; i < G / 32; ++i) {
+                            // (the 16-byte pieces in an order that keeps 8 tokens off each other's banks)
+                            const int ch = (i + (tok >> (C::ROW == 64 ? 1 : 2))) & (G / 32 - 1);
+                            const uint4 v = lds128(src + ch * 16);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                sts128(dst + (ch * 4 + t) * (TOK * 16), w[t] & 0x000f000fu, w[t] & 0x00f000f0u,
+                                       (w[t] >> 8) & 0x000f000fu, (w[t] >> 8) & 0x00f000f0u);
+                        }
+                    } else {
+                        // exponents of the tile: each warp looks at all of its tokens
+                        int top0 = -24, top1 = -24;
+                        bool bad_value = false;
+#pragma unroll
+                        for (int i = 0; i < TOK * GR / 32; ++i) {
+                            const int k = i * 32 + lane, kt = k % TOK;
+                            const float2 x = unpack_f16(lds32(raw + TOK * C::ROW + kt * C::PAR + 4 * (k / TOK)));
+                            if (tok0 + kt <= g.hi && !((s_bad[stage] >> (kt / align)) & 1u)) {
+                                const bool fin = fabsf(x.x) <= 65504.0f && fabsf(x.y) <= 65504.0f;
+                                bad_value |= !fin;
+                                if (fin) {
+                                    top0 = max(top0, exp_of(x.x));
+                                    top1 = max(top1, exp_of(x.y));
+                                }
+                            }
+                        }
+                        top0 = __reduce_max_sync(0xffffffffu, top0);
+                        top1 = __reduce_max_sync(0xffffffffu, top1);
+                        bad_value = __any_sync(0xffffffffu, bad_value);
+                        if (j == 0 || top0 > e0 + 5) e0 = top0 - 3;
+                        if (j == 0 || top1 > e1 + 14) e1 = top1 - 10;
+                        float2 x = unpack_f16(lds32(raw + TOK * C::ROW + tok * C::PAR + 4 * r));
+                        float mu = 1.0f, inv = 0.0f, lm = 0.0f;
+                        uint32_t mult = 0, less = 0, mult16 = 0, less16 = 0;  // 2^k, -2^(k + 10), 2^(k - 4), -2^(k + 6)
+                        if (held && !gone) {
+                            if (!(fabsf(x.x) <= 65504.0f && fabsf(x.y) <= 65504.0f)) {
+                                mu = __int_as_float(0x7fffffff);
+                            } else {
+                                // a step far below e0's takes part of its exponent into the weight; what would
+                                // leave fp16 even so (below 2^-20 of the largest step) counts as 0
+                                const int k = max(exp_of(x.x) - e0, -20);
+                                mu = x.x * pow2i(-k - e0);
+                                inv = __fdividef(1.0f, mu);
+                                lm = x.y * pow2i(-e1);
+                                if (fabsf(inv) <= 32768.0f && fabsf(lm * inv) <= 32768.0f) {
+                                    lm *= inv;
+                                    const float b = pow2i(k);
+                                    mult = pack_f16(b, b);
+                                    less = pack_f16(b * -1024.0f, b * -1024.0f);
+                                    mult16 = pack_f16(b * 0.0625f, b * 0.0625f);
+                                    less16 = pack_f16(b * -64.0f, b * -64.0f);
+                                } else {
+                                    mu = inv = 1.0f;
+                                }
+                            }
+                        }
+                        sts32f(par + ((2 * GR + r) * TOK + tok) * 4, mu);
+                        const uint32_t vb = base + C::OFF_V + buf * C::VB + r * (G / 8 + 2) * (TOK * 16) + tok * 16;
+                        {
+                            const uint32_t hi = pack_f16(inv, lm);
+                            const float2 h = unpack_f16(hi);
+                            const uint32_t lo = pack_f16(inv - h.x, lm - h.y);
+                            sts128(vb + (G / 8) * (TOK * 16), __byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632), 0, 0);
+                        }
+                        if (warp == 8 && lane == 0) s_info[buf] = {e0, e1, bad_value ? 1 : 0};
+                        auto scaled = [](uint32_t v, uint32_t by, uint32_t minus) {
+                            uint32_t d;
+                            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v | 0x64006400u), "r"(by), "r"(minus));
+                            return d;
+                        };
+#pragma unroll
+                        for (int i = 0; i < G / 32; ++i) {
+                            const int ch = (i + (tok >> (C::ROW == 64 ? 1 : 2))) & (G / 32 - 1);
+                            const uint4 v = lds128(src + ch * 16);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                sts128(vb + (ch * 4 + t) * (TOK * 16), scaled(w[t] & 0x000f000fu, mult, less),
+                                       scaled(w[t] & 0x00f000f0u, mult16, less16),
+                                       scaled((w[t] >> 8) & 0x000f000fu, mult, less),
+                                       scaled((w[t] >> 8) & 0x00f000f0u, mult16, less16));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(RAW_EMPTY + stage));
+                        mbar_arrive(bar(KV_FULL + buf));
+                    }
+                }
+            }
+        } else if (warp == 14) {
+            // =============================================================== products
+            uint32_t n = 0, np[2] = {0, 0}, segs[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](int i, uint32_t parity) {
+                ok = ok && mbar_wait(bar(i), parity & 1, abort, status, SITE_KV4_ATTENTION);
+                ok = __all_sync(0xffffffffu, ok);
+                return ok;
+            };
+            const uint64_t kd = desc_plain(base + C::OFF_K, TOK * 16, 128);
+            const uint64_t vd = desc_plain(base + C::OFF_V, 128, TOK * 16);
+            const uint64_t qd = desc_plain(base + C::OFF_Q, kRows * 16, 128);
+            auto scores = [&](int tile, int buf) {
+                if (lane != 0) return;
+#pragma unroll
+                for (int r = 0; r < GR; ++r)
+#pragma unroll
+                    for (int k = 0; k < G / 16; ++k)
+                        mma_ss(tmem + tile * SC + r * TOK, qd + ((tile * C::QB + (r * (G / 16) + k) * 2 * kRows * 16) >> 4),
+                               kd + ((buf * C::KB + (r * (G / 16) + k) * 2 * TOK * 16) >> 4), idesc_f16(TOK, false), k > 0);
+                tc_commit(bar(S_FULL + tile));
+            };
+            auto outputs = [&](int tile, int buf, bool more) {
+                if (lane != 0) return;
+#pragma unroll
+                for (int r = 0; r < GR; ++r)
+#pragma unroll
+                    for (int k = 0; k < TOK / 16; ++k)
+                        mma_ts(tmem + C::T_O + tile * OC + r * (G + 16), tmem + tile * SC + r * (TOK / 2) + 8 * k,
+                               vd + ((buf * C::VB + r * (G / 8 + 2) * TOK * 16 + k * 256) >> 4), idesc_f16(G + 16, true),
+                               more || k > 0);
+            };
+            while (ok && next()) {
+                if (g.tiles <= 0) continue;
+                const int tiles2 = g.ncols > kRows ? 2 : 1;
+                for (int t = 0; t < tiles2; ++t) wait(Q_FULL + t, segs[t]++);
+                wait(KV_FULL + (n & 1), n >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int t = 0; t < tiles2; ++t) scores(t, n & 1);
+                for (int j = 0; j < g.tiles && ok; ++j, ++n) {
+                    for (int t = 0; t < tiles2; ++t) {
+                        if (!wait(P_FULL + t, np[t]++)) break;
+                        tc_fence_after();
+                        outputs(t, n & 1, j > 0);
+                        if (lane == 0) {
+                            if (j + 1 == g.tiles) tc_commit(bar(O_FULL + t));
+                            if (t == tiles2 - 1) tc_commit(bar(KV_EMPTY + (n & 1)));
+                        }
+                        __syncwarp();
+                        if (j + 1 < g.tiles) {
+                            if (t == 0) {
+                                if (!wait(KV_FULL + ((n + 1) & 1), (n + 1) >> 1)) break;
+                                tc_fence_after();
+                            }
+                            scores(t, (n + 1) & 1);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            // every product has ended before TMEM is given back
+            if (lane == 0) {
+                tc_commit(bar(DRAIN));
+                mbar_drain(bar(DRAIN), 0, kWaitLimitNs);
+            }
+            __syncwarp();
+        } else {
+            // =============================================================== copies
+            uint32_t n = 0;
+            bool ok = true;
+            while (ok && next()) {
+                if (g.tiles <= 0) continue;
+                const int step = GR == 2 || small_pages ? 16 : 32;  // tokens of a copy
+                const int groups = TOK / step;
+                const int grp = lane >> 2, what = lane & 3;  // K codes, K parameters, V codes, V parameters
+                for (int j = 0; j < g.tiles; ++j, ++n) {
+                    const int stage = n % kRing;
+                    const int at = g.start + (g.tile0 + j) * TOK + grp * step;
+                    int64_t src = -1;
+                    bool bad = false;
+                    if (grp < groups && at <= g.hi) {
+                        const int pg = __ldg(a.pool.table + static_cast<int64_t>(g.b) * a.pool.table_ld + (at >> page_log2));
+                        bad = pg < 0 || pg >= a.pool.pages;
+                        if (!bad)
+                            src = static_cast<int64_t>(pg) * a.pool.page_stride +
+                                  static_cast<int64_t>(g.head) * a.pool.block_bytes;
+                    }
+                    if (bad) report(status, BQ_ERR_INVALID_ARG, SITE_KV4_ATTENTION);
+                    ok = n < kRing || mbar_wait(bar(RAW_EMPTY + stage), (n / kRing - 1) & 1, abort, status, SITE_KV4_ATTENTION);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t good = __ballot_sync(0xffffffffu, src >= 0 && what == 0);
+                    const uint32_t bads = __ballot_sync(0xffffffffu, bad && what == 0);
+                    if (lane == 0) {
+                        uint32_t bits = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) bits |= ((bads >> (4 * i)) & 1u) << i;
+                        s_bad[stage] = bits;
+                        mbar_arrive_expect_tx(bar(RAW_FULL + stage),
+                                              static_cast<uint32_t>(__popc(good) * step * 2 * (C::ROW + C::PAR)));
+                    }
+                    __syncwarp();
+                    if (src >= 0) {
+                        const int slot = at & ((1 << page_log2) - 1);
+                        const int off = (what >> 1) * static_cast<int>(a.pool.block_bytes >> 1) +
+                                        ((what & 1) ? (C::ROW << page_log2) + slot * C::PAR : slot * C::ROW);
+                        const uint32_t dst = base + C::OFF_RAW + stage * C::RAW + (what >> 1) * (TOK * (C::ROW + C::PAR)) +
+                                             ((what & 1) ? TOK * C::ROW + grp * step * C::PAR : grp * step * C::ROW);
+                        bulk_load(dst, a.pool.pool + src + off,
+                                  static_cast<uint32_t>(step * ((what & 1) ? C::PAR : C::ROW)), bar(RAW_FULL + stage));
+                    }
+                    __syncwarp();
+                }
+            }
+            // copies still in flight land before the CTA ends
+            for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
+                mbar_drain(bar(RAW_FULL + i % kRing), (i / kRing) & 1, kWaitLimitNs);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 14) tmem_dealloc(tmem, 512);
+}
+
+template <typename C, bool MODS, typename T>
+cudaError_t launch_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {
+    auto kern = kv4_prefill_kernel<C, MODS, T>;
+    static SmemOptIn opt_in;
+    cudaError_t e = smem_opt_in(opt_in, dev, reinterpret_cast<const void *>(kern), static_cast<size_t>(C::SMEM));
+    if (e != cudaSuccess) return e;
+    // the register split of the roles adds up to what a CTA is launched with
+    static const int regs = [&] {
+        cudaFuncAttributes f = {};
+        return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs < 121) return cudaErrorInvalidConfiguration;
+    const unsigned grid = static_cast<unsigned>(std::min(dev.num_sms, kKv4MaxSms));
+    const Kv4Ws ws = kv4_workspace(a.workspace);
+    kern<<<grid, kPThreads, C::SMEM, s>>>(a, ws, dev.status);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : kv4_launch_join<C::D, C::G, kCols, T>(a, ws, grid, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {
+    auto by_shape = [&](auto tag) {
+        using T = decltype(tag);
+        const bool mods = a.softcap > 0.0f || a.slopes != nullptr;
+        auto go = [&](auto c) {
+            using C = decltype(c);
+            return mods ? launch_prefill<C, true, T>(a, s, dev) : launch_prefill<C, false, T>(a, s, dev);
+        };
+        if (a.pool.head_dim == 64) return go(PShape<64, 64>());
+        return a.pool.group_size == 64 ? go(PShape<128, 64>()) : go(PShape<128, 128>());
+    };
+    return a.dtype == BQ_F16 ? by_shape(__half()) : by_shape(__nv_bfloat16());
+}
+
+}  // namespace bq
