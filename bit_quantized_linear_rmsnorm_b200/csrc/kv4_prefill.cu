@@ -38,6 +38,7 @@
 // Every wait is bounded; if one runs out the kernel records BQ_ERR_TIMEOUT,
 // lets its copies and products end (bounded again) and finishes.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4_attention.cuh"
 
@@ -46,7 +47,8 @@ namespace {
 
 constexpr int kRows = 128;     // of a tile
 constexpr int kCols = 256;     // columns of an item
-constexpr int kPThreads = 512;
+constexpr int kPThreads = 768;
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 88, kOtherRegs = 64;  // registers: 512 x 88 + 256 x 64 = 768 x 80
 constexpr int kRing = 3;       // raw stages
 constexpr float kRise = 7.0f;  // the running maximum is raised when passed by more
 constexpr int kOverhead = 192; // cost of starting an item, in tokens
@@ -75,10 +77,42 @@ struct PShape {
     static_assert(T_O + 2 * OC <= 512, "TMEM");
 };
 
+// Bounded wait of a role: polls at the hardware's own pace and looks at the
+// clock now and then only, since the warps that work share its issue slots.
+__device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status,
+                                          uint32_t site) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (i & 63u) continue;
+        if (*abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            report(status, BQ_ERR_TIMEOUT, site);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool elect_one() {  // one lane of a converged warp
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// A row of the tiles, for the lanes that hold its scores; then what they found.
+struct RowInfo {
+    float f, sq[2], slope;
+    int pos, finite;
+    float m, sum;
+};
+
 // What a tile of tokens tells the softmax beside its parameters.
 struct TileInfo {
-    int e0, e1;
-    int odd;  // holds values that are not finite
+    int ue, uo;  // O holds the sums of even dims times 2^-ue, of odd dims times 2^-uo
+    int e1;      // and L the minima's times 2^-e1
+    int odd;     // holds values that are not finite
 };
 
 __device__ __forceinline__ uint64_t pack64(float lo, float hi) {
@@ -107,8 +141,10 @@ __device__ __forceinline__ float pow2i(int e) {  // 2^e, 0 below 2^-126
 __device__ __forceinline__ int exp_of(float x) {  // of a finite x; 2^-24 and less give -24
     return max(static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127, -24);
 }
-__device__ __forceinline__ void lds128(uint32_t a, uint64_t &x, uint64_t &y) {
-    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+__device__ __forceinline__ uint64_t lds64x(uint32_t a) {
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a));
+    return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -155,18 +191,43 @@ __device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t *r) {
     else
         tmem_ld_32x32b_x16(a, *reinterpret_cast<uint32_t(*)[16]>(r));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+// 16 lanes x 8 N columns as the fragments of a matrix product: of each 8
+// columns, lane 4 g + t holds columns 2 t, 2 t + 1 of rows g and g + 8.
+template <int N>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t a, uint32_t *r);
+template <>
+__device__ __forceinline__ void tmem_ld_rows<2>(uint32_t a, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a)
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(a),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+template <>
+__device__ __forceinline__ void tmem_ld_rows<4>(uint32_t a, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(a)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_rows(uint32_t a, const uint32_t *r);
+template <>
+__device__ __forceinline__ void tmem_st_rows<2>(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// 16 lanes x 4 N columns: of each 4, lane 4 g + t holds column t of rows g, g + 8.
+template <int N>
+__device__ __forceinline__ void tmem_st_half(uint32_t a, const uint32_t *r);
+template <>
+__device__ __forceinline__ void tmem_st_half<2>(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st_half<4>(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 template <int N>
@@ -282,7 +343,8 @@ enum Bar {
     P_FULL = S_FULL + 2,
     Q_FULL = P_FULL + 2,
     O_FULL = Q_FULL + 2,
-    DRAIN = O_FULL + 2,
+    PAIR = O_FULL + 2,  // the two warps of 32 rows
+    DRAIN = PAIR + 8,
     kBars = DRAIN + 1
 };
 
@@ -298,9 +360,12 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
     __shared__ int64_t s_sum[kPThreads / 32];
     __shared__ int64_t s_before;
     __shared__ int s_b;
+    __shared__ RowInfo s_rows[kCols];
     pdl_launch_dependents();  // the joining kernel waits for this grid before it reads
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t base = smem_u32(smem), bars = smem_u32(s_bars);
+    const uint32_t base = smem_u32(smem);
+    uint32_t bars = smem_u32(s_bars);
+    asm volatile("" : "+r"(bars));  // (kept, not worked out again in every poll)
     const int share = a.q_heads / a.pool.kv_heads, H = a.pool.kv_heads, page_log2 = a.pool.page_log2;
     auto bar = [&](int i) { return bars + 8 * i; };
 
@@ -345,7 +410,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             at += n;
         }
     }
-    if (warp == 14) {
+    if (warp == 22) {
         tmem_alloc(smem_u32(&s_tmem), 512);
         tmem_relinquish();
     }
@@ -353,7 +418,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
         for (int i = 0; i < kBars; ++i)
             mbar_init(bar(i), i >= RAW_EMPTY && i < KV_FULL ? 6
                               : i >= KV_FULL && i < KV_EMPTY ? 6
-                              : (i >= P_FULL && i < O_FULL) ? 4 : 1);
+                              : i >= P_FULL && i < O_FULL ? 8 : i >= PAIR && i < DRAIN ? 2 : 1);
         fence_mbarrier_init();
     }
     // the columns of [O | L] behind the sums stay zero
@@ -367,7 +432,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
     tc_fence_after();
     walk.b = s_b;
     walk.seq_begin = s_before;
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = 0;  // (all 512 columns are this CTA's, so they begin at 0)
     volatile int *abort = &s_abort;
     Segment g;
     // tiles start at a multiple of what one copy takes
@@ -376,23 +441,32 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
         return GR == 2 || small_pages ? next_segment<TOK, 16>(a, share, walk, g) : next_segment<TOK, 32>(a, share, walk, g);
     };
 
-    if (warp < 8) {
-        regs_inc<184>();
+    if (warp < 16) {
+        regs_inc<kSoftmaxRegs>();
         // =================================================================== softmax
-        const int tile = warp >> 2, wl = warp & 3, row = threadIdx.x & 127;
-        const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
+        // warp 8 tile + 4 hw + wl: rows 32 wl + 16 hw + 0..15 of the tile (wl: the quarter of TMEM that it reaches)
+        const int tile = warp >> 3, hw = warp >> 2 & 1, wl = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(32 * wl + 16 * hw) << 16;
         const uint32_t ts = tmem + tile * SC + lanes, to = tmem + C::T_O + tile * OC + lanes;
         uint32_t n = 0;        // tiles so far, of all items (buffers)
         uint32_t mine_n = 0;   // tiles so far of this tile of rows
-        uint32_t segs = 0;
+        uint32_t segs = 0, meets = 0;
         bool ok = true;
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(PAIR + tile * 4 + wl));
+            ok = wait_role(bar(PAIR + tile * 4 + wl), meets++ & 1, abort, status, SITE_KV4_ATTENTION);
+            ok = __all_sync(0xffffffffu, ok);
+            return ok;
+        };
         while (ok && next()) {
             if (g.tiles <= 0) {
                 // a share that ends before the first tile of what it holds: nothing to add
                 float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4));
-                const int c = tile * kRows + row;
-                slot[c * (D + 4) + D] = kNoMax;
-                slot[c * (D + 4) + D + 1] = 0.0f;
+                if (threadIdx.x < kCols) {
+                    slot[threadIdx.x * (D + 4) + D] = kNoMax;
+                    slot[threadIdx.x * (D + 4) + D + 1] = 0.0f;
+                }
             }
             if (g.begins && !g.whole && threadIdx.x == 0) {
                 const int64_t last = (g.end * ctas - 1) / total;  // CTA that holds the item's end
@@ -403,24 +477,24 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 n += g.tiles;
                 continue;
             }
-            const int c = tile * kRows + row;
-            const bool on = c < g.ncols;
-            const int qrow = (g.col0 + c) / share, hh = (g.col0 + c) - qrow * share;
-            const int pos = on ? g.pos0 + qrow : -1;
-            bool finite = true;
-            float f, sq[GR], slope2 = 0.0f;
+            if (!meet()) break;  // (the other warp of these 32 rows has read what the last item left)
             {
+                // two lanes to a row, half of the dims each
+                const int row = 32 * wl + 16 * hw + (lane >> 1), part = lane & 1, c = tile * kRows + row;
+                const bool on = c < g.ncols;
+                const int qrow = (g.col0 + c) / share, hh = (g.col0 + c) - qrow * share;
                 const T *q = static_cast<const T *>(a.q) + (g.first + qrow) * a.q_tok +
-                             (static_cast<int64_t>(g.head) * share + hh) * a.q_head;
+                             (static_cast<int64_t>(g.head) * share + hh) * a.q_head + part * (D / 2);
+                bool finite = true;
                 float top = 0.0f;
-                uint4 raw[D / 8];
+                uint4 raw[D / 16];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int i = 0; i < D / 16; ++i) {
                     raw[i] = make_uint4(0, 0, 0, 0);
                     if (on) raw[i] = __ldg(reinterpret_cast<const uint4 *>(q) + i);
                 }
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int i = 0; i < D / 16; ++i) {
                     float x[8];
                     Kv4In<T>::unpack(*reinterpret_cast<const uint4(*)[1]>(&raw[i]), x);
 #pragma unroll
@@ -429,33 +503,37 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         finite &= fabsf(x[j]) <= 3.402823466e38f;
                     }
                 }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                finite &= __shfl_xor_sync(0xffffffffu, finite ? 1 : 0, 1) != 0;
                 // 2^k brings the row's largest into [2^14, 2^15); a negative scale turns the row
                 int k = top > 0.0f && finite ? 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127) : 0;
                 k = min(k, 120);
                 const float up = !finite ? 0.0f : copysignf(__uint_as_float(static_cast<uint32_t>(127 + k) << 23), a.scale);
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                const bool capped = MODS && a.softcap > 0.0f;
-                f = fabsf(a.scale) * 1.4426950408889634f * down * 16777216.0f;  // codes are c 2^-24
-                if (capped) f *= 2.0f / a.softcap;  // the argument of tanh, times 2 log2(e)
-                const uint32_t dst = base + C::OFF_Q + tile * C::QB + row * 16;
+                float f = fabsf(a.scale) * 1.4426950408889634f * down * 16777216.0f;  // codes are c 2^-24
+                if (MODS && a.softcap > 0.0f) f *= 2.0f / a.softcap;  // the argument of tanh, times 2 log2(e)
+                const uint32_t dst = base + C::OFF_Q + tile * C::QB + part * (D / 16) * (kRows * 16) + row * 16;
+                float sq = 0.0f;
 #pragma unroll
-                for (int r = 0; r < GR; ++r) sq[r] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int i = 0; i < D / 16; ++i) {
                     float x[8];
                     Kv4In<T>::unpack(*reinterpret_cast<const uint4(*)[1]>(&raw[i]), x);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         x[j] = finite ? x[j] * up : 0.0f;
-                        sq[i / (G / 8)] += x[j];
+                        sq += x[j];
                     }
                     sts128(dst + i * (kRows * 16), pack_f16(x[0], x[4]), pack_f16(x[1] * 0.0625f, x[5] * 0.0625f),
                            pack_f16(x[2], x[6]), pack_f16(x[3] * 0.0625f, x[7] * 0.0625f));
                 }
-#pragma unroll
-                for (int r = 0; r < GR; ++r) sq[r] *= 5.9604644775390625e-08f;  // 2^-24, as f has 2^24
-                if (MODS && a.slopes != nullptr && on)
-                    slope2 = __ldg(a.slopes + g.head * share + hh) * 1.4426950408889634f;
+                sq *= 5.9604644775390625e-08f;  // 2^-24, as f has 2^24
+                const float other = __shfl_xor_sync(0xffffffffu, sq, 1);
+                if (part == 0) {
+                    float slope = 0.0f;
+                    if (MODS && a.slopes != nullptr && on)
+                        slope = __ldg(a.slopes + g.head * share + hh) * 1.4426950408889634f;
+                    s_rows[c] = {f, {GR == 1 ? sq + other : sq, other}, slope, on ? g.pos0 + qrow : -1, finite ? 1 : 0, 0.0f, 0.0f};
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -465,16 +543,31 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             const int row_hi = (g.col0 + min(g.ncols, (tile + 1) * kRows) - 1) / share;
             const int all_hi = min(g.pos0 + row_lo, g.hi);  // positions that every row of the tile sees
             const int all_lo = a.window > 0 ? g.pos0 + row_hi - a.window + 1 : 0;
-            const int64_t see_lo = a.window > 0 ? static_cast<int64_t>(pos) - a.window + 1 : 0;
 
-            float m = kNoMax, sum = 0.0f;  // sum: of the weights, kept where it is asked for
-            int e0 = 0, e1 = 0;
+            // scores are held as a product's fragments: rows 8 i + g4 (i = 0, 1) of the warp's 16, tokens 8 b + 2 t4
+            // and + 1 of a tile: a thread reads a quarter of the tokens' parameters (read by rows, they would take
+            // as much of the shared memory's time as the products take)
+            const int g4 = lane >> 2, t4 = lane & 3;
+            RowInfo *rows = s_rows + tile * kRows + 32 * wl + 16 * hw + g4;
+            float f[2], sq[2][GR], slope2[2], m[2], sum[2];  // sum: of the weights, kept where it is asked for
+            int pos[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[i] = rows[8 * i].f;
+#pragma unroll
+                for (int r = 0; r < GR; ++r) sq[i][r] = rows[8 * i].sq[r];
+                slope2[i] = MODS ? rows[8 * i].slope : 0.0f;
+                pos[i] = rows[8 * i].pos;
+                m[i] = kNoMax;
+                sum[i] = 0.0f;
+            }
+            int ue = 0, uo = 0, e1 = 0;
             for (int j = 0; j < g.tiles; ++j) {
                 const int tok0 = g.start + (g.tile0 + j) * TOK;
                 const int buf = n & 1;
                 // (S first: these threads may have left tiles out that are not theirs, and S tells that KV_FULL is at n)
-                ok = mbar_wait(bar(S_FULL + tile), mine_n & 1, abort, status, SITE_KV4_ATTENTION);
-                ok = ok && mbar_wait(bar(KV_FULL + buf), (n >> 1) & 1, abort, status, SITE_KV4_ATTENTION);
+                ok = wait_role(bar(S_FULL + tile), mine_n & 1, abort, status, SITE_KV4_ATTENTION);
+                ok = ok && wait_role(bar(KV_FULL + buf), (n >> 1) & 1, abort, status, SITE_KV4_ATTENTION);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -483,144 +576,171 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 const TileInfo info = s_info[buf];
                 const bool edge = tok0 + TOK - 1 > all_hi || tok0 < all_lo || info.odd != 0;
                 const uint32_t par = base + C::OFF_P + buf * C::PB;
-                uint64_t y[TOK / 2];  // pairs of tokens
+                constexpr int NB = TOK / 8;
+                uint64_t y[NB][2];  // pairs of tokens 8 b + 2 t4, + 1 of row 8 i + g4
                 if constexpr (GR == 1) {
+                    tmem_ld_rows<4>(ts, reinterpret_cast<uint32_t *>(y[0]));
 #pragma unroll
-                    for (int i = 0; i < TOK; i += 32) tmem_ld<32>(ts + i, reinterpret_cast<uint32_t *>(y) + i);
-                    tmem_wait_ld();
-                    const uint64_t sq2 = pack64(sq[0], sq[0]);
+                    for (int b0 = 0; b0 < NB; b0 += 4) {  // four blocks at a time, the next on its way
+                        tmem_wait_ld();
+                        if (b0 + 4 < NB) tmem_ld_rows<4>(ts + 8 * (b0 + 4), reinterpret_cast<uint32_t *>(y[b0 + 4]));
 #pragma unroll
-                    for (int i = 0; i < TOK / 4; ++i) {
-                        uint64_t s0, s1, m0, m1;
-                        lds128(par + 16 * i, s0, s1);
-                        lds128(par + TOK * 4 + 16 * i, m0, m1);
-                        y[2 * i] = fma2(y[2 * i], s0, mul2(m0, sq2));
-                        y[2 * i + 1] = fma2(y[2 * i + 1], s1, mul2(m1, sq2));
+                        for (int b = b0; b < b0 + 4; ++b) {
+                            const uint64_t s2 = lds64x(par + (8 * b + 2 * t4) * 4);
+                            const uint64_t m2 = lds64x(par + (TOK + 8 * b + 2 * t4) * 4);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                y[b][i] = fma2(y[b][i], s2, mul2(m2, pack64(sq[i][0], sq[i][0])));
+                        }
                     }
                 } else {
-                    const uint64_t sq2 = pack64(sq[0], sq[0]), sr2 = pack64(sq[1], sq[1]);
 #pragma unroll
-                    for (int h = 0; h < TOK; h += 16) {
-                        uint64_t u[8];
-                        tmem_ld<16>(ts + h, reinterpret_cast<uint32_t *>(y) + h);
-                        tmem_ld<16>(ts + TOK + h, reinterpret_cast<uint32_t *>(u));
+                    for (int b0 = 0; b0 < NB; b0 += 2) {
+                        uint64_t u[2][2];
+                        tmem_ld_rows<2>(ts + 8 * b0, reinterpret_cast<uint32_t *>(y[b0]));
+                        tmem_ld_rows<2>(ts + TOK + 8 * b0, reinterpret_cast<uint32_t *>(u[0]));
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = h / 4; i < h / 4 + 4; ++i) {
-                            uint64_t s0, s1, m0, m1, t0, t1, n0, n1;
-                            lds128(par + 16 * i, s0, s1);
-                            lds128(par + TOK * 4 + 16 * i, t0, t1);
-                            lds128(par + TOK * 8 + 16 * i, m0, m1);
-                            lds128(par + TOK * 12 + 16 * i, n0, n1);
-                            y[2 * i] = fma2(y[2 * i], s0, fma2(u[2 * i - h / 2], t0, fma2(n0, sr2, mul2(m0, sq2))));
-                            y[2 * i + 1] =
-                                fma2(y[2 * i + 1], s1, fma2(u[2 * i + 1 - h / 2], t1, fma2(n1, sr2, mul2(m1, sq2))));
+                        for (int b = b0; b < b0 + 2; ++b) {
+                            const uint32_t at = par + (8 * b + 2 * t4) * 4;
+                            const uint64_t s2 = lds64x(at), v2 = lds64x(at + TOK * 4);
+                            const uint64_t m2 = lds64x(at + TOK * 8), n2 = lds64x(at + TOK * 12);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                y[b][i] = fma2(y[b][i], s2,
+                                               fma2(u[b - b0][i], v2, fma2(n2, pack64(sq[i][GR - 1], sq[i][GR - 1]),
+                                                                           mul2(m2, pack64(sq[i][0], sq[i][0])))));
                         }
                     }
                 }
-                const uint32_t mu = par + 2 * GR * TOK * 4;
+                const uint32_t mu = par + (2 * GR * TOK + 2 * t4) * 4;
 
                 if constexpr (MODS) {  // scores in powers of two from here on
-                    const uint64_t f2 = pack64(f, f);
                     const float cap2 = a.softcap * 1.4426950408889634f;
-                    const float away = static_cast<float>(tok0 - pos);
 #pragma unroll
-                    for (int i = 0; i < TOK / 2; ++i) {
-                        float2 z = unpack64(mul2(y[i], f2));
-                        if (a.softcap > 0.0f) {  // cap tanh(x) = cap (1 - 2 / (exp(2 x) + 1))
-                            z.x = fmaf(-2.0f * cap2, rcp(ex2(z.x) + 1.0f), cap2);
-                            z.y = fmaf(-2.0f * cap2, rcp(ex2(z.y) + 1.0f), cap2);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint64_t f2 = pack64(f[i], f[i]);
+                        const float away = static_cast<float>(tok0 + 2 * t4 - pos[i]);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            float2 z = unpack64(mul2(y[b][i], f2));
+                            if (a.softcap > 0.0f) {  // cap tanh(x) = cap (1 - 2 / (exp(2 x) + 1))
+                                z.x = fmaf(-2.0f * cap2, rcp(ex2(z.x) + 1.0f), cap2);
+                                z.y = fmaf(-2.0f * cap2, rcp(ex2(z.y) + 1.0f), cap2);
+                            }
+                            z.x = fmaf(slope2[i], away + static_cast<float>(8 * b), z.x);
+                            z.y = fmaf(slope2[i], away + static_cast<float>(8 * b + 1), z.y);
+                            y[b][i] = pack64(z.x, z.y);
                         }
-                        z.x = fmaf(slope2, away + static_cast<float>(2 * i), z.x);
-                        z.y = fmaf(slope2, away + static_cast<float>(2 * i + 1), z.y);
-                        y[i] = pack64(z.x, z.y);
                     }
                 }
-                uint32_t seen[(TOK + 31) / 32];
+                int see_lo[2], see_hi[2];  // first and last token that the row sees, from 2 t4 of the tile on
                 if (edge) {
 #pragma unroll
-                    for (int w = 0; w < (TOK + 31) / 32; ++w) {
-                        const int64_t lo = max(see_lo - tok0 - 32 * w, int64_t(0));
-                        const int64_t hi = min(static_cast<int64_t>(min(pos, g.hi)) - tok0 - 32 * w, int64_t(31));
-                        seen[w] = hi < lo ? 0u : (0xffffffffu >> (31 - static_cast<int>(hi))) & (0xffffffffu << static_cast<int>(lo));
-                    }
+                    for (int i = 0; i < 2; ++i) {
+                        see_hi[i] = min(pos[i], g.hi) - tok0 - 2 * t4;
+                        see_lo[i] = a.window > 0 ? max(pos[i] - a.window + 1, 0) - tok0 - 2 * t4 : -TOK;
 #pragma unroll
-                    for (int i = 0; i < TOK / 2; ++i) {
-                        const float2 z = unpack64(y[i]);
-                        y[i] = pack64((seen[i / 16] >> (2 * i % 32)) & 1u ? z.x : kNoMax,
-                                      (seen[i / 16] >> (2 * i % 32 + 1)) & 1u ? z.y : kNoMax);
-                    }
-                }
-                float top = kNoMax;
-#pragma unroll
-                for (int i = 0; i < TOK / 2; ++i) {
-                    const float2 z = unpack64(y[i]);
-                    top = fmaxf(top, fmaxf(z.x, z.y));
-                }
-                if (!MODS) top = fmaxf(top * f, kNoMax);
-
-                const bool rise = top > m + kRise;
-                if (__any_sync(0xffffffffu, rise) || (j > 0 && (info.e0 != e0 || info.e1 != e1))) {
-                    const float now = fmaxf(m, top), keep = ex2(m - now);
-                    m = now;
-                    sum *= keep;
-                    if (j > 0) {  // (the products up to here are complete: S came after them)
-                        const float ko = keep * pow2i(e0 - info.e0), km = keep * pow2i(e1 - info.e1);
-#pragma unroll
-                        for (int i = 0; i < OC; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld<16>(to + i, o);
-                            tmem_wait_ld();
-                            const bool sums = i % (G + 16) == G;
-#pragma unroll
-                            for (int t = 0; t < 16; ++t) {
-                                const float by = sums ? (t < 2 ? keep : km) : ko;
-                                o[t] = __float_as_uint(__uint_as_float(o[t]) * by);
-                            }
-                            tmem_st16(to + i, o);
+                        for (int b = 0; b < NB; ++b) {
+                            float2 z = unpack64(y[b][i]);
+                            if (8 * b > see_hi[i] || 8 * b < see_lo[i]) z.x = kNoMax;
+                            if (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i]) z.y = kNoMax;
+                            y[b][i] = pack64(z.x, z.y);
                         }
                     }
                 }
-                e0 = info.e0;
+                float top[2];
+                bool rise = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top[i] = kNoMax;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const float2 z = unpack64(y[b][i]);
+                        top[i] = fmaxf(top[i], fmaxf(z.x, z.y));
+                    }
+                    if (!MODS) top[i] = fmaxf(top[i] * f[i], kNoMax);
+                    rise |= top[i] > m[i] + kRise;
+                }
+                if (__any_sync(0xffffffffu, rise) || (j > 0 && (info.ue != ue || info.uo != uo || info.e1 != e1))) {
+                    float keep[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+                        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+                        const float now = fmaxf(m[i], top[i]);
+                        keep[i] = ex2(m[i] - now);
+                        m[i] = now;
+                        sum[i] *= keep[i];
+                    }
+                    if (j > 0) {  // (the products up to here are complete: S came after them)
+                        // columns 2 t4, 2 t4 + 1 of 8: dims t4 and t4 + 4; of the sums: the divisor's, the minima's
+                        const float ko = t4 & 1 ? pow2i(uo - info.uo) : pow2i(ue - info.ue);
+                        const float ks = t4 == 0 ? 1.0f : pow2i(e1 - info.e1);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < OC; c0 += 16) {
+                            uint32_t o[8];
+                            const float by = c0 % (G + 16) == G ? ks : ko;
+                            tmem_ld_rows<2>(to + c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int t = 0; t < 8; ++t)
+                                o[t] = __float_as_uint(__uint_as_float(o[t]) * (by * keep[t >> 1 & 1]));
+                            tmem_st_rows<2>(to + c0, o);
+                        }
+                    }
+                }
+                ue = info.ue;
+                uo = info.uo;
                 e1 = info.e1;
 
-                const uint64_t f2 = MODS ? pack64(1.0f, 1.0f) : pack64(f, f);
-                const uint64_t off2 = pack64(kLift - m, kLift - m);
 #pragma unroll
-                for (int i = 0; i < TOK / 2; ++i) {
-                    const float2 x = unpack64(fma2(y[i], f2, off2));
-                    y[i] = pack64(ex2(x.x), ex2(x.y));
+                for (int i = 0; i < 2; ++i) {
+                    const float f1 = MODS ? 1.0f : f[i];
+                    const uint64_t f2 = pack64(f1, f1), off2 = pack64(kLift - m[i], kLift - m[i]);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const float2 x = unpack64(fma2(y[b][i], f2, off2));
+                        y[b][i] = pack64(ex2(x.x), ex2(x.y));
+                    }
                 }
                 if (a.lse != nullptr) {
 #pragma unroll
-                    for (int i = 0; i < TOK / 2; ++i) {
-                        const uint32_t bits = edge ? seen[i / 16] >> (2 * i % 32) : 3u;
-                        const float2 x = unpack64(y[i]);
-                        sum += (bits & 1u ? x.x : 0.0f) + (bits & 2u ? x.y : 0.0f);
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            float2 x = unpack64(y[b][i]);
+                            if (edge && (8 * b > see_hi[i] || 8 * b < see_lo[i])) x.x = 0.0f;
+                            if (edge && (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i])) x.y = 0.0f;
+                            sum[i] += x.x + x.y;
+                        }
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < GR; ++r) {
+                    uint32_t w[NB][2];
 #pragma unroll
-                    for (int h = 0; h < TOK; h += 16) {
-                        uint32_t w[8];
+                    for (int b = 0; b < NB; ++b) {
+                        const uint64_t m2 = lds64x(mu + (r * TOK + 8 * b) * 4);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint64_t m0, m1;
-                            lds128(mu + (r * TOK + h + 4 * i) * 4, m0, m1);
-                            float2 x0 = unpack64(mul2(y[h / 2 + 2 * i], m0)), x1 = unpack64(mul2(y[h / 2 + 2 * i + 1], m1));
-                            if (edge) {
-                                const uint32_t bits = seen[h / 32] >> (h % 32 + 4 * i);
-                                x0.x = bits & 1u ? x0.x : 0.0f;
-                                x0.y = bits & 2u ? x0.y : 0.0f;
-                                x1.x = bits & 4u ? x1.x : 0.0f;
-                                x1.y = bits & 8u ? x1.y : 0.0f;
-                            }
-                            w[2 * i] = pack_f16(x0.x, x0.y);
-                            w[2 * i + 1] = pack_f16(x1.x, x1.y);
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 x = unpack64(mul2(y[b][i], m2));
+                            w[b][i] = pack_f16(x.x, x.y);
                         }
-                        tmem_st8(ts + r * (TOK / 2) + h / 2, w);
                     }
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                if (8 * b > see_hi[i] || 8 * b < see_lo[i]) w[b][i] &= 0xffff0000u;
+                                if (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i]) w[b][i] &= 0xffffu;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b + 4 <= NB; b += 4) tmem_st_half<4>(ts + r * (TOK / 2) + 4 * b, w[b]);
+                    if constexpr (NB % 4 != 0) tmem_st_half<2>(ts + r * (TOK / 2) + 4 * (NB / 4 * 4), w[NB / 4 * 4]);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -630,85 +750,114 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 ++mine_n;
             }
             if (!ok) break;
-            ok = mbar_wait(bar(O_FULL + tile), segs & 1, abort, status, SITE_KV4_ATTENTION);
+            ok = wait_role(bar(O_FULL + tile), segs & 1, abort, status, SITE_KV4_ATTENTION);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
             ++segs;
             tc_fence_after();
-            // ---- results
-            const float w0 = pow2i(e0), w1 = pow2i(e1);
-            const bool spoilt = pos >= 0 && (!finite || pos >= g.cap);
-            if (pos >= g.cap) report(status, BQ_ERR_INVALID_ARG, SITE_KV4_ATTENTION);
-            const int64_t row_out = (g.first + qrow) * a.q_heads + static_cast<int64_t>(g.head) * share + hh;
-            float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4)) + c * (D + 4);
+            // ---- results: a thread per row, half of the dims for each of the two warps of 32 rows
 #pragma unroll
-            for (int r = 0; r < GR; ++r) {
+            for (int i = 0; i < 2; ++i) {
+                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+                if (t4 == 0) {
+                    rows[8 * i].m = m[i];
+                    rows[8 * i].sum = sum[i];
+                }
+            }
+            if (!meet()) break;
+            {
+                const int c = tile * kRows + 32 * wl + lane;
+                const bool on = c < g.ncols;
+                const int qrow = (g.col0 + c) / share, hh = (g.col0 + c) - qrow * share;
+                const RowInfo row = s_rows[c];
+                const bool spoilt = row.pos >= 0 && (!row.finite || row.pos >= g.cap);
+                if (row.pos >= g.cap) report(status, BQ_ERR_INVALID_ARG, SITE_KV4_ATTENTION);
+                const float we = pow2i(ue), wo = pow2i(uo), w1 = pow2i(e1);
+                const int64_t row_out = (g.first + qrow) * a.q_heads + static_cast<int64_t>(g.head) * share + hh;
+                float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4)) + c * (D + 4);
+                const uint32_t ot = tmem + C::T_O + tile * OC + (static_cast<uint32_t>(32 * wl) << 16);
+                const int grp = GR == 1 ? 0 : hw;
                 uint32_t l[16];
-                tmem_ld<16>(to + r * (G + 16) + G, l);
+                tmem_ld<16>(ot + grp * (G + 16) + G, l);
                 tmem_wait_ld();
-                float den = __uint_as_float(l[0]) + __uint_as_float(l[1]);
+                float den = __uint_as_float(l[0]) + __uint_as_float(l[1]), row_sum = row.sum;
                 const float lm = (__uint_as_float(l[2]) + __uint_as_float(l[3])) * w1;
-                if (a.lse == nullptr && r == 0) sum = den;
-                if (spoilt) den = sum = __int_as_float(0x7fffffff);
+                if (a.lse == nullptr) row_sum = den;
+                if (spoilt) den = row_sum = __int_as_float(0x7fffffff);
                 const float inv = !g.whole ? 1.0f : den == 0.0f ? 0.0f : __fdividef(1.0f, den);
+                const int d0 = hw * (D / 2);
 #pragma unroll
-                for (int h = 0; h < G; h += 16) {
+                for (int h = 0; h < D / 2; h += 16) {
                     uint32_t o[16];
-                    tmem_ld<16>(to + r * (G + 16) + h, o);
+                    tmem_ld<16>(ot + (GR == 1 ? d0 : grp * (G + 16)) + h, o);
                     tmem_wait_ld();
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {  // columns 0..7 of a block are dims 0 4 1 5 2 6 3 7
                         const int d = (i & 8) + ((i & 1) << 2) + ((i & 7) >> 1);
-                        v[d] = fmaf(__uint_as_float(o[i]), w0, lm) * inv;
+                        v[d] = fmaf(__uint_as_float(o[i]), (i & 2) ? wo : we, lm) * inv;
                     }
-                    if (on) {
-                        if (g.whole) {
-                            uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row_out * D + r * G + h);
-                            out[0] = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
-                                                pack2(v[6], v[7], T()));
-                            out[1] = make_uint4(pack2(v[8], v[9], T()), pack2(v[10], v[11], T()), pack2(v[12], v[13], T()),
-                                                pack2(v[14], v[15], T()));
-                        } else {
-                            float4 *out = reinterpret_cast<float4 *>(slot + r * G + h);
+                    if (on && g.whole) {
+                        uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row_out * D + d0 + h);
+                        out[0] = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
+                                            pack2(v[6], v[7], T()));
+                        out[1] = make_uint4(pack2(v[8], v[9], T()), pack2(v[10], v[11], T()), pack2(v[12], v[13], T()),
+                                            pack2(v[14], v[15], T()));
+                    } else if (on) {
+                        float4 *out = reinterpret_cast<float4 *>(slot + d0 + h);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                out[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            out[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     }
                 }
                 if (on && !g.whole) {
-                    if (r == 0) {
-                        slot[D] = m;
-                        slot[D + 1] = sum;
+                    if (hw == 0) {
+                        slot[D] = row.m;
+                        slot[D + 1] = row_sum;
                     }
-                    slot[D + 2 + r] = den;
+                    if (hw < GR) slot[D + 2 + hw] = den;
                 }
-                if (on && g.whole && r == 0 && a.lse != nullptr)
-                    a.lse[row_out] = sum == 0.0f ? -INFINITY : (m - kLift + log2f(sum)) * 0.6931471805599453f;
+                if (on && g.whole && hw == 0 && a.lse != nullptr)
+                    a.lse[row_out] = row_sum == 0.0f ? -INFINITY : (row.m - kLift + log2f(row_sum)) * 0.6931471805599453f;
             }
             tc_fence_before();
         }
     } else {
-        regs_dec<72>();
-        if (warp < 14) {
+        regs_dec<kOtherRegs>();
+        if (warp < 22) {
             // =============================================================== unpacking
-            const bool values = warp < 11;
-            const int u = (static_cast<int>(threadIdx.x) - (values ? 256 : 352));
+            const bool values = warp < 19;
+            const int u = (static_cast<int>(threadIdx.x) - (values ? 512 : 608));
             const int tok = u % TOK, r = u / TOK;  // token and group of this thread
             uint32_t n = 0;
             int e0 = 0, e1 = 0;
+            bool near = true;  // the value steps are all within 2^9 of each other
             bool ok = true;
+            // codes as fp16 subnormals, masked in place
+            auto codes = [&](uint32_t src, uint32_t dst) {
+#pragma unroll
+                for (int i = 0; i < G / 32; ++i) {
+                    // (the 16-byte pieces in an order that keeps 8 tokens off each other's banks)
+                    const int ch = (i + (tok >> (C::ROW == 64 ? 1 : 2))) & (G / 32 - 1);
+                    const uint4 v = lds128(src + ch * 16);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        sts128(dst + (ch * 4 + t) * (TOK * 16), w[t] & 0x000f000fu, w[t] & 0x00f000f0u,
+                               (w[t] >> 8) & 0x000f000fu, (w[t] >> 8) & 0x00f000f0u);
+                }
+            };
             while (ok && next()) {
                 if (g.tiles <= 0) continue;
                 const int align = GR == 2 || small_pages ? 16 : 32;
                 for (int j = 0; j < g.tiles; ++j, ++n) {
                     const int stage = n % kRing, buf = n & 1;
                     const int tok0 = g.start + (g.tile0 + j) * TOK;
-                    ok = n < 2 || mbar_wait(bar(KV_EMPTY + buf), ((n >> 1) - 1) & 1, abort, status, SITE_KV4_ATTENTION);
-                    ok = ok && mbar_wait(bar(RAW_FULL + stage), (n / kRing) & 1, abort, status, SITE_KV4_ATTENTION);
+                    ok = n < 2 || wait_role(bar(KV_EMPTY + buf), ((n >> 1) - 1) & 1, abort, status, SITE_KV4_ATTENTION);
+                    ok = ok && wait_role(bar(RAW_FULL + stage), (n / kRing) & 1, abort, status, SITE_KV4_ATTENTION);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
@@ -724,52 +873,64 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         if (gone) x.x = __int_as_float(0x7fffffff);
                         sts32f(par + (r * TOK + tok) * 4, x.x);
                         sts32f(par + ((GR + r) * TOK + tok) * 4, x.y);
-                        const uint32_t dst = base + C::OFF_K + buf * C::KB + r * (G / 8) * (TOK * 16) + tok * 16;
-#pragma unroll
-                        for (int i = 0; i < G / 32; ++i) {
-                            // (the 16-byte pieces in an order that keeps 8 tokens off each other's banks)
-                            const int ch = (i + (tok >> (C::ROW == 64 ? 1 : 2))) & (G / 32 - 1);
-                            const uint4 v = lds128(src + ch * 16);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                sts128(dst + (ch * 4 + t) * (TOK * 16), w[t] & 0x000f000fu, w[t] & 0x00f000f0u,
-                                       (w[t] >> 8) & 0x000f000fu, (w[t] >> 8) & 0x00f000f0u);
-                        }
+                        codes(src, base + C::OFF_K + buf * C::KB + r * (G / 8) * (TOK * 16) + tok * 16);
                     } else {
-                        // exponents of the tile: each warp looks at all of its tokens
-                        int top0 = -24, top1 = -24;
-                        bool bad_value = false;
+                        // exponents of the tile (fp16's fields): each warp looks at all of its tokens
+                        uint32_t hi_s = 0, lo_s = 0x7c00u, hi_m = 0;
 #pragma unroll
                         for (int i = 0; i < TOK * GR / 32; ++i) {
                             const int k = i * 32 + lane, kt = k % TOK;
-                            const float2 x = unpack_f16(lds32(raw + TOK * C::ROW + kt * C::PAR + 4 * (k / TOK)));
+                            const uint32_t w = lds32(raw + TOK * C::ROW + kt * C::PAR + 4 * (k / TOK));
+                            const uint32_t fs = w & 0x7c00u, fm = (w >> 16) & 0x7c00u;
                             if (tok0 + kt <= g.hi && !((s_bad[stage] >> (kt / align)) & 1u)) {
-                                const bool fin = fabsf(x.x) <= 65504.0f && fabsf(x.y) <= 65504.0f;
-                                bad_value |= !fin;
-                                if (fin) {
-                                    top0 = max(top0, exp_of(x.x));
-                                    top1 = max(top1, exp_of(x.y));
+                                hi_s = max(hi_s, fs == 0x7c00u || fm == 0x7c00u ? 0x8000u : fs);
+                                if (fs != 0x7c00u && fm != 0x7c00u) {
+                                    lo_s = min(lo_s, fs);
+                                    hi_m = max(hi_m, fm);
                                 }
                             }
                         }
-                        top0 = __reduce_max_sync(0xffffffffu, top0);
-                        top1 = __reduce_max_sync(0xffffffffu, top1);
-                        bad_value = __any_sync(0xffffffffu, bad_value);
-                        if (j == 0 || top0 > e0 + 5) e0 = top0 - 3;
-                        if (j == 0 || top1 > e1 + 14) e1 = top1 - 10;
-                        float2 x = unpack_f16(lds32(raw + TOK * C::ROW + tok * C::PAR + 4 * r));
-                        float mu = 1.0f, inv = 0.0f, lm = 0.0f;
-                        uint32_t mult = 0, less = 0, mult16 = 0, less16 = 0;  // 2^k, -2^(k + 10), 2^(k - 4), -2^(k + 6)
-                        if (held && !gone) {
-                            if (!(fabsf(x.x) <= 65504.0f && fabsf(x.y) <= 65504.0f)) {
-                                mu = __int_as_float(0x7fffffff);
-                            } else {
+                        hi_s = __reduce_max_sync(0xffffffffu, hi_s);
+                        lo_s = __reduce_min_sync(0xffffffffu, lo_s);
+                        hi_m = __reduce_max_sync(0xffffffffu, hi_m);
+                        const bool odd = hi_s == 0x8000u;
+                        if (odd) {  // the largest of the finite ones
+                            hi_s = 0;
+#pragma unroll 1
+                            for (int i = 0; i < TOK * GR / 32; ++i) {
+                                const int k = i * 32 + lane, kt = k % TOK;
+                                const uint32_t w = lds32(raw + TOK * C::ROW + kt * C::PAR + 4 * (k / TOK));
+                                if (tok0 + kt <= g.hi && (w & 0x7c00u) != 0x7c00u) hi_s = max(hi_s, w & 0x7c00u);
+                            }
+                            hi_s = __reduce_max_sync(0xffffffffu, hi_s);
+                        }
+                        const int top0 = static_cast<int>(hi_s >> 10) - 15, top1 = static_cast<int>(hi_m >> 10) - 15;
+                        if (j == 0) near = true;
+                        if (j == 0 || top1 > e1 + 4) e1 = top1 - 2;
+                        if (near) {
+                            if (j == 0 || top0 > e0) e0 = top0 + 1;
+                            near = lo_s == 0x7c00u || (lo_s != 0 && static_cast<int>(lo_s >> 10) - 15 >= e0 - 9);
+                        }
+                        if (!near && (j == 0 || top0 > e0 + 5)) e0 = top0 - 3;
+                        const float2 x = unpack_f16(lds32(raw + TOK * C::ROW + tok * C::PAR + 4 * r));
+                        const uint32_t vb = base + C::OFF_V + buf * C::VB + r * (G / 8 + 2) * (TOK * 16) + tok * 16;
+                        const bool fit = held && !gone && fabsf(x.x) <= 65504.0f && fabsf(x.y) <= 65504.0f;
+                        float mu = held && !gone && !fit ? __int_as_float(0x7fffffff) : 1.0f, inv = 0.0f, lm = 0.0f;
+                        if (near) {
+                            if (fit) {
+                                mu = x.x * pow2i(-e0);
+                                inv = rcp(mu);
+                                lm = x.y * pow2i(-e1) * inv;
+                            }
+                            codes(src, vb);
+                        } else {
+                            uint32_t mult = 0, less = 0, mult16 = 0, less16 = 0;  // 2^k, -2^(k + 10), 2^(k - 4), -2^(k + 6)
+                            if (fit) {
                                 // a step far below e0's takes part of its exponent into the weight; what would
                                 // leave fp16 even so (below 2^-20 of the largest step) counts as 0
                                 const int k = max(exp_of(x.x) - e0, -20);
                                 mu = x.x * pow2i(-k - e0);
-                                inv = __fdividef(1.0f, mu);
+                                inv = rcp(mu);
                                 lm = x.y * pow2i(-e1);
                                 if (fabsf(inv) <= 32768.0f && fabsf(lm * inv) <= 32768.0f) {
                                     lm *= inv;
@@ -782,33 +943,25 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                                     mu = inv = 1.0f;
                                 }
                             }
+                            auto scaled = [](uint32_t v, uint32_t by, uint32_t minus) {
+                                uint32_t d;
+                                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v | 0x64006400u), "r"(by), "r"(minus));
+                                return d;
+                            };
+#pragma unroll 1
+                            for (int i = 0; i < G / 8; ++i) {
+                                const uint32_t w = lds32(src + 4 * i);
+                                sts128(vb + i * (TOK * 16), scaled(w & 0x000f000fu, mult, less),
+                                       scaled(w & 0x00f000f0u, mult16, less16), scaled((w >> 8) & 0x000f000fu, mult, less),
+                                       scaled((w >> 8) & 0x00f000f0u, mult16, less16));
+                            }
                         }
                         sts32f(par + ((2 * GR + r) * TOK + tok) * 4, mu);
-                        const uint32_t vb = base + C::OFF_V + buf * C::VB + r * (G / 8 + 2) * (TOK * 16) + tok * 16;
-                        {
-                            const uint32_t hi = pack_f16(inv, lm);
-                            const float2 h = unpack_f16(hi);
-                            const uint32_t lo = pack_f16(inv - h.x, lm - h.y);
-                            sts128(vb + (G / 8) * (TOK * 16), __byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632), 0, 0);
-                        }
-                        if (warp == 8 && lane == 0) s_info[buf] = {e0, e1, bad_value ? 1 : 0};
-                        auto scaled = [](uint32_t v, uint32_t by, uint32_t minus) {
-                            uint32_t d;
-                            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v | 0x64006400u), "r"(by), "r"(minus));
-                            return d;
-                        };
-#pragma unroll
-                        for (int i = 0; i < G / 32; ++i) {
-                            const int ch = (i + (tok >> (C::ROW == 64 ? 1 : 2))) & (G / 32 - 1);
-                            const uint4 v = lds128(src + ch * 16);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                sts128(vb + (ch * 4 + t) * (TOK * 16), scaled(w[t] & 0x000f000fu, mult, less),
-                                       scaled(w[t] & 0x00f000f0u, mult16, less16),
-                                       scaled((w[t] >> 8) & 0x000f000fu, mult, less),
-                                       scaled((w[t] >> 8) & 0x00f000f0u, mult16, less16));
-                        }
+                        const uint32_t hi = pack_f16(inv, lm);
+                        const float2 h = unpack_f16(hi);
+                        const uint32_t lo = pack_f16(inv - h.x, lm - h.y);
+                        sts128(vb + (G / 8) * (TOK * 16), __byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632), 0, 0);
+                        if (warp == 16 && lane == 0) s_info[buf] = {near ? e0 + 24 : e0, near ? e0 + 20 : e0, e1, odd ? 1 : 0};
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -818,69 +971,90 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                     }
                 }
             }
-        } else if (warp == 14) {
+        } else if (warp == 22) {
             // =============================================================== products
             uint32_t n = 0, np[2] = {0, 0}, segs[2] = {0, 0};
             bool ok = true;
             auto wait = [&](int i, uint32_t parity) {
-                ok = ok && mbar_wait(bar(i), parity & 1, abort, status, SITE_KV4_ATTENTION);
+                ok = ok && wait_role(bar(i), parity & 1, abort, status, SITE_KV4_ATTENTION);
                 ok = __all_sync(0xffffffffu, ok);
                 return ok;
             };
-            const uint64_t kd = desc_plain(base + C::OFF_K, TOK * 16, 128);
-            const uint64_t vd = desc_plain(base + C::OFF_V, 128, TOK * 16);
-            const uint64_t qd = desc_plain(base + C::OFF_Q, kRows * 16, 128);
-            auto scores = [&](int tile, int buf) {
-                if (lane != 0) return;
+            // (tile and buffer are constants of each copy of this code, so that descriptors and addresses are
+            // uniform: a product then issues in the time that the one before it takes)
+            auto scores = [&](auto tile_, auto buf_) {
+                constexpr int tile = decltype(tile_)::value, buf = decltype(buf_)::value;
+                if (!elect_one()) return;
+                const uint64_t qd = desc_plain(base + C::OFF_Q + tile * C::QB, kRows * 16, 128);
+                const uint64_t kd = desc_plain(base + C::OFF_K + buf * C::KB, TOK * 16, 128);
 #pragma unroll
                 for (int r = 0; r < GR; ++r)
 #pragma unroll
                     for (int k = 0; k < G / 16; ++k)
-                        mma_ss(tmem + tile * SC + r * TOK, qd + ((tile * C::QB + (r * (G / 16) + k) * 2 * kRows * 16) >> 4),
-                               kd + ((buf * C::KB + (r * (G / 16) + k) * 2 * TOK * 16) >> 4), idesc_f16(TOK, false), k > 0);
+                        mma_ss(tile * SC + r * TOK, qd + (((r * (G / 16) + k) * 2 * kRows * 16) >> 4),
+                               kd + (((r * (G / 16) + k) * 2 * TOK * 16) >> 4), idesc_f16(TOK, false), k > 0);
                 tc_commit(bar(S_FULL + tile));
             };
-            auto outputs = [&](int tile, int buf, bool more) {
-                if (lane != 0) return;
+            auto outputs = [&](auto tile_, auto buf_, bool more, bool end, bool done) {
+                constexpr int tile = decltype(tile_)::value, buf = decltype(buf_)::value;
+                if (!elect_one()) return;
+                const uint64_t vd = desc_plain(base + C::OFF_V + buf * C::VB, 128, TOK * 16);
 #pragma unroll
                 for (int r = 0; r < GR; ++r)
 #pragma unroll
                     for (int k = 0; k < TOK / 16; ++k)
-                        mma_ts(tmem + C::T_O + tile * OC + r * (G + 16), tmem + tile * SC + r * (TOK / 2) + 8 * k,
-                               vd + ((buf * C::VB + r * (G / 8 + 2) * TOK * 16 + k * 256) >> 4), idesc_f16(G + 16, true),
-                               more || k > 0);
+                        mma_ts(C::T_O + tile * OC + r * (G + 16), tile * SC + r * (TOK / 2) + 8 * k,
+                               vd + ((r * (G / 8 + 2) * TOK * 16 + k * 256) >> 4), idesc_f16(G + 16, true), more || k > 0);
+                if (end) tc_commit(bar(O_FULL + tile));
+                if (done) tc_commit(bar(KV_EMPTY + buf));
+            };
+            constexpr std::integral_constant<int, 0> c0;
+            constexpr std::integral_constant<int, 1> c1;
+            // products of tile n of the tokens, in buffer `buf`, and the scores of the next
+            auto step = [&](auto buf, auto other, bool first, bool last, bool two) {
+                if (!wait(P_FULL, np[0]++)) return;
+                tc_fence_after();
+                outputs(c0, buf, !first, last, !two);
+                __syncwarp();
+                if (!last) {
+                    if (!wait(KV_FULL + decltype(other)::value, (n + 1) >> 1)) return;
+                    tc_fence_after();
+                    scores(c0, other);
+                    __syncwarp();
+                }
+                if (!two) return;
+                if (!wait(P_FULL + 1, np[1]++)) return;
+                tc_fence_after();
+                outputs(c1, buf, !first, last, true);
+                __syncwarp();
+                if (!last) scores(c1, other);
+                __syncwarp();
             };
             while (ok && next()) {
                 if (g.tiles <= 0) continue;
-                const int tiles2 = g.ncols > kRows ? 2 : 1;
-                for (int t = 0; t < tiles2; ++t) wait(Q_FULL + t, segs[t]++);
+                const bool two = g.ncols > kRows;
+                wait(Q_FULL, segs[0]++);
+                if (two) wait(Q_FULL + 1, segs[1]++);
                 wait(KV_FULL + (n & 1), n >> 1);
                 if (!ok) break;
                 tc_fence_after();
-                for (int t = 0; t < tiles2; ++t) scores(t, n & 1);
+                if (n & 1) {
+                    scores(c0, c1);
+                    if (two) scores(c1, c1);
+                } else {
+                    scores(c0, c0);
+                    if (two) scores(c1, c0);
+                }
+                __syncwarp();
                 for (int j = 0; j < g.tiles && ok; ++j, ++n) {
-                    for (int t = 0; t < tiles2; ++t) {
-                        if (!wait(P_FULL + t, np[t]++)) break;
-                        tc_fence_after();
-                        outputs(t, n & 1, j > 0);
-                        if (lane == 0) {
-                            if (j + 1 == g.tiles) tc_commit(bar(O_FULL + t));
-                            if (t == tiles2 - 1) tc_commit(bar(KV_EMPTY + (n & 1)));
-                        }
-                        __syncwarp();
-                        if (j + 1 < g.tiles) {
-                            if (t == 0) {
-                                if (!wait(KV_FULL + ((n + 1) & 1), (n + 1) >> 1)) break;
-                                tc_fence_after();
-                            }
-                            scores(t, (n + 1) & 1);
-                        }
-                        __syncwarp();
-                    }
+                    if (n & 1)
+                        step(c1, c0, j == 0, j + 1 == g.tiles, two);
+                    else
+                        step(c0, c1, j == 0, j + 1 == g.tiles, two);
                 }
             }
             // every product has ended before TMEM is given back
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_commit(bar(DRAIN));
                 mbar_drain(bar(DRAIN), 0, kWaitLimitNs);
             }
@@ -907,7 +1081,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                                   static_cast<int64_t>(g.head) * a.pool.block_bytes;
                     }
                     if (bad) report(status, BQ_ERR_INVALID_ARG, SITE_KV4_ATTENTION);
-                    ok = n < kRing || mbar_wait(bar(RAW_EMPTY + stage), (n / kRing - 1) & 1, abort, status, SITE_KV4_ATTENTION);
+                    ok = n < kRing || wait_role(bar(RAW_EMPTY + stage), (n / kRing - 1) & 1, abort, status, SITE_KV4_ATTENTION);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
@@ -943,7 +1117,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 14) tmem_dealloc(tmem, 512);
+    if (warp == 22) tmem_dealloc(s_tmem, 512);
 }
 
 template <typename C, bool MODS, typename T>
@@ -957,7 +1131,7 @@ cudaError_t launch_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &
         cudaFuncAttributes f = {};
         return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
     }();
-    if (regs < 121) return cudaErrorInvalidConfiguration;
+    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(std::min(dev.num_sms, kKv4MaxSms));
     const Kv4Ws ws = kv4_workspace(a.workspace);
     kern<<<grid, kPThreads, C::SMEM, s>>>(a, ws, dev.status);
