@@ -77,13 +77,13 @@ struct PShape {
     static_assert(T_O + 2 * OC <= 512, "TMEM");
 };
 
-// Bounded wait of a role: polls at the hardware's own pace and looks at the
-// clock now and then only, since the warps that work share its issue slots.
+// Bounded wait of a role: the warps that work share its issue slots, so it
+// looks at the clock only when it has not been woken.
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status,
                                           uint32_t site) {
+    if (mbar_try_wait(bar, parity)) return true;
     uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if (i & 63u) continue;
+    while (!mbar_try_wait_sleep(bar, parity)) {
         if (*abort) return false;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
@@ -272,23 +272,22 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int sha
     return w;
 }
 
-// The parts of items that make up a CTA's share, one after the other; every
-// role walks them by itself.
+// The parts of items that make up a CTA's share, one after the other: the
+// copying warp works them out and hands them to the others.
 struct Segment {
     int b, head, col0, ncols;
-    int start, hi;     // first token of the first tile, last token that is read (-1: none)
-    int tile0, tiles;  // tiles of this part
+    int start, hi;     // first token of the part, last token that is read (-1: none)
+    int tiles;         // of this part; 0 behind the last part
     int pos0, cap;
     int64_t first;
     bool begins, whole;
-    int64_t end;       // of the item, in the list
 };
 struct Walk {
     int64_t at, stop, seq_begin;
     int b;
 };
 template <int TOK, int ALIGN>
-__device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, Walk &w, Segment &s) {
+__device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, Walk &w, Segment &s, int64_t &end) {
     if (w.at >= w.stop) return false;
     SeqWork q = seq_work(a, w.b, share);
     while (w.at >= w.seq_begin + q.cost * a.pool.kv_heads) {
@@ -306,7 +305,7 @@ __device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, Wa
             hi = mid - 1;
     }
     const int64_t begin = w.seq_begin + head * q.cost + cost_upto(q, lo);
-    s.end = w.seq_begin + head * q.cost + cost_upto(q, lo + 1);
+    end = w.seq_begin + head * q.cost + cost_upto(q, lo + 1);
     s.b = w.b;
     s.head = static_cast<int>(head);
     s.col0 = static_cast<int>(lo) * kCols;
@@ -325,11 +324,12 @@ __device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, Wa
     } else {
         tiles = (s.hi - s.start) / TOK + 1;
     }
-    const int64_t stop = min(s.end, w.stop), cost = s.end - begin;
-    s.tile0 = static_cast<int>((w.at - begin) * tiles / cost);
-    s.tiles = static_cast<int>(stop == s.end ? tiles : (stop - begin) * tiles / cost) - s.tile0;
+    const int64_t stop = min(end, w.stop), cost = end - begin;
+    const int tile0 = static_cast<int>((w.at - begin) * tiles / cost);
+    s.tiles = static_cast<int>(stop == end ? tiles : (stop - begin) * tiles / cost) - tile0;
+    s.start += tile0 * TOK;
     s.begins = w.at == begin;
-    s.whole = s.begins && stop == s.end;
+    s.whole = s.begins && stop == end;
     w.at = stop;
     return true;
 }
@@ -344,7 +344,9 @@ enum Bar {
     Q_FULL = P_FULL + 2,
     O_FULL = Q_FULL + 2,
     PAIR = O_FULL + 2,  // the two warps of 32 rows
-    DRAIN = PAIR + 8,
+    SEG_FULL = PAIR + 8,
+    SEG_EMPTY = SEG_FULL + 2,
+    DRAIN = SEG_EMPTY + 2,
     kBars = DRAIN + 1
 };
 
@@ -361,6 +363,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
     __shared__ int64_t s_before;
     __shared__ int s_b;
     __shared__ RowInfo s_rows[kCols];
+    __shared__ Segment s_seg[2];
     pdl_launch_dependents();  // the joining kernel waits for this grid before it reads
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
         for (int i = 0; i < kBars; ++i)
             mbar_init(bar(i), i >= RAW_EMPTY && i < KV_FULL ? 6
                               : i >= KV_FULL && i < KV_EMPTY ? 6
-                              : i >= P_FULL && i < O_FULL ? 8 : i >= PAIR && i < DRAIN ? 2 : 1);
+                              : i >= P_FULL && i < O_FULL ? 8 : i >= PAIR && i < SEG_FULL ? 2 : i >= SEG_EMPTY && i < DRAIN ? 23 : 1);
         fence_mbarrier_init();
     }
     // the columns of [O | L] behind the sums stay zero
@@ -430,16 +433,23 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    walk.b = s_b;
-    walk.seq_begin = s_before;
     const uint32_t tmem = 0;  // (all 512 columns are this CTA's, so they begin at 0)
     volatile int *abort = &s_abort;
-    Segment g;
-    // tiles start at a multiple of what one copy takes
-    const bool small_pages = page_log2 == 4;
-    auto next = [&]() {
-        return GR == 2 || small_pages ? next_segment<TOK, 16>(a, share, walk, g) : next_segment<TOK, 32>(a, share, walk, g);
+    // tokens of a copy; tiles start at a multiple of it
+    const int step = GR == 2 || page_log2 == 4 ? 16 : 32;
+
+    // The next part for a warp that is done with the one before it.
+    uint32_t parts = 0;
+    auto next_part = [&](Segment &g) {
+        __syncwarp();
+        if (parts > 0 && lane == 0) mbar_arrive(bar(SEG_EMPTY + ((parts - 1) & 1)));
+        const bool ok = wait_role(bar(SEG_FULL + (parts & 1)), (parts >> 1) & 1, abort, status, SITE_KV4_ATTENTION);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        g = s_seg[parts & 1];
+        ++parts;
+        return g.tiles > 0;
     };
+    Segment g;
 
     if (warp < 16) {
         regs_inc<kSoftmaxRegs>();
@@ -459,20 +469,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             ok = __all_sync(0xffffffffu, ok);
             return ok;
         };
-        while (ok && next()) {
-            if (g.tiles <= 0) {
-                // a share that ends before the first tile of what it holds: nothing to add
-                float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4));
-                if (threadIdx.x < kCols) {
-                    slot[threadIdx.x * (D + 4) + D] = kNoMax;
-                    slot[threadIdx.x * (D + 4) + D + 1] = 0.0f;
-                }
-            }
-            if (g.begins && !g.whole && threadIdx.x == 0) {
-                const int64_t last = (g.end * ctas - 1) / total;  // CTA that holds the item's end
-                ws.desc[cta] = {g.first, g.col0, g.ncols, g.head, static_cast<int>(last - cta) + 1};
-            }
-            if (g.tiles <= 0) continue;
+        while (ok && next_part(g)) {
             if (tile * kRows >= g.ncols) {  // no rows for this tile
                 n += g.tiles;
                 continue;
@@ -563,7 +560,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             }
             int ue = 0, uo = 0, e1 = 0;
             for (int j = 0; j < g.tiles; ++j) {
-                const int tok0 = g.start + (g.tile0 + j) * TOK;
+                const int tok0 = g.start + j * TOK;
                 const int buf = n & 1;
                 // (S first: these threads may have left tiles out that are not theirs, and S tells that KV_FULL is at n)
                 ok = wait_role(bar(S_FULL + tile), mine_n & 1, abort, status, SITE_KV4_ATTENTION);
@@ -850,12 +847,10 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                                (w[t] >> 8) & 0x000f000fu, (w[t] >> 8) & 0x00f000f0u);
                 }
             };
-            while (ok && next()) {
-                if (g.tiles <= 0) continue;
-                const int align = GR == 2 || small_pages ? 16 : 32;
+            while (ok && next_part(g)) {
                 for (int j = 0; j < g.tiles; ++j, ++n) {
                     const int stage = n % kRing, buf = n & 1;
-                    const int tok0 = g.start + (g.tile0 + j) * TOK;
+                    const int tok0 = g.start + j * TOK;
                     ok = n < 2 || wait_role(bar(KV_EMPTY + buf), ((n >> 1) - 1) & 1, abort, status, SITE_KV4_ATTENTION);
                     ok = ok && wait_role(bar(RAW_FULL + stage), (n / kRing) & 1, abort, status, SITE_KV4_ATTENTION);
                     if (!__all_sync(0xffffffffu, ok)) {
@@ -865,7 +860,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                     const uint32_t raw = base + C::OFF_RAW + stage * C::RAW + (values ? TOK * (C::ROW + C::PAR) : 0);
                     const uint32_t par = base + C::OFF_P + buf * C::PB;
                     const bool held = tok0 + tok <= g.hi;
-                    const bool gone = (s_bad[stage] >> (tok / align)) & 1u;
+                    const bool gone = (s_bad[stage] >> (tok / step)) & 1u;
                     const uint32_t src = raw + tok * C::ROW + r * (G / 2);
                     if (!values) {
                         float2 x = unpack_f16(lds32(raw + TOK * C::ROW + tok * C::PAR + 4 * r));
@@ -882,7 +877,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                             const int k = i * 32 + lane, kt = k % TOK;
                             const uint32_t w = lds32(raw + TOK * C::ROW + kt * C::PAR + 4 * (k / TOK));
                             const uint32_t fs = w & 0x7c00u, fm = (w >> 16) & 0x7c00u;
-                            if (tok0 + kt <= g.hi && !((s_bad[stage] >> (kt / align)) & 1u)) {
+                            if (tok0 + kt <= g.hi && !((s_bad[stage] >> (kt / step)) & 1u)) {
                                 hi_s = max(hi_s, fs == 0x7c00u || fm == 0x7c00u ? 0x8000u : fs);
                                 if (fs != 0x7c00u && fm != 0x7c00u) {
                                     lo_s = min(lo_s, fs);
@@ -1011,7 +1006,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             constexpr std::integral_constant<int, 0> c0;
             constexpr std::integral_constant<int, 1> c1;
             // products of tile n of the tokens, in buffer `buf`, and the scores of the next
-            auto step = [&](auto buf, auto other, bool first, bool last, bool two) {
+            auto products = [&](auto buf, auto other, bool first, bool last, bool two) {
                 if (!wait(P_FULL, np[0]++)) return;
                 tc_fence_after();
                 outputs(c0, buf, !first, last, !two);
@@ -1030,8 +1025,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 if (!last) scores(c1, other);
                 __syncwarp();
             };
-            while (ok && next()) {
-                if (g.tiles <= 0) continue;
+            while (ok && next_part(g)) {
                 const bool two = g.ncols > kRows;
                 wait(Q_FULL, segs[0]++);
                 if (two) wait(Q_FULL + 1, segs[1]++);
@@ -1048,9 +1042,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 __syncwarp();
                 for (int j = 0; j < g.tiles && ok; ++j, ++n) {
                     if (n & 1)
-                        step(c1, c0, j == 0, j + 1 == g.tiles, two);
+                        products(c1, c0, j == 0, j + 1 == g.tiles, two);
                     else
-                        step(c0, c1, j == 0, j + 1 == g.tiles, two);
+                        products(c0, c1, j == 0, j + 1 == g.tiles, two);
                 }
             }
             // every product has ended before TMEM is given back
@@ -1063,14 +1057,40 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             // =============================================================== copies
             uint32_t n = 0;
             bool ok = true;
-            while (ok && next()) {
-                if (g.tiles <= 0) continue;
-                const int step = GR == 2 || small_pages ? 16 : 32;  // tokens of a copy
+            walk.b = s_b;
+            walk.seq_begin = s_before;
+            while (ok) {
+                int64_t end = 0;
+                const bool more = step == 16 ? next_segment<TOK, 16>(a, share, walk, g, end)
+                                             : next_segment<TOK, 32>(a, share, walk, g, end);
+                if (!more) g.tiles = 0;
+                if (more && g.begins && !g.whole && lane == 0) {
+                    const int64_t last = (end * ctas - 1) / total;  // CTA that holds the item's end
+                    ws.desc[cta] = {g.first, g.col0, g.ncols, g.head, static_cast<int>(last - cta) + 1};
+                }
+                if (more && g.tiles <= 0) {
+                    // a share that ends before the first tile of what it holds: nothing to add
+                    float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4));
+                    for (int c = lane; c < kCols; c += 32) {
+                        slot[c * (D + 4) + D] = kNoMax;
+                        slot[c * (D + 4) + D + 1] = 0.0f;
+                    }
+                    continue;
+                }
+                ok = parts < 2 || wait_role(bar(SEG_EMPTY + (parts & 1)), ((parts >> 1) - 1) & 1, abort, status, SITE_KV4_ATTENTION);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lane == 0) {
+                    s_seg[parts & 1] = g;
+                    mbar_arrive(bar(SEG_FULL + (parts & 1)));
+                }
+                __syncwarp();
+                ++parts;
+                if (!more) break;
                 const int groups = TOK / step;
                 const int grp = lane >> 2, what = lane & 3;  // K codes, K parameters, V codes, V parameters
                 for (int j = 0; j < g.tiles; ++j, ++n) {
                     const int stage = n % kRing;
-                    const int at = g.start + (g.tile0 + j) * TOK + grp * step;
+                    const int at = g.start + j * TOK + grp * step;
                     int64_t src = -1;
                     bool bad = false;
                     if (grp < groups && at <= g.hi) {
