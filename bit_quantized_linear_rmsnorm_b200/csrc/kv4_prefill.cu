@@ -77,17 +77,29 @@ struct PShape {
     static_assert(T_O + 2 * OC <= 512, "TMEM");
 };
 
-// Bounded wait of a role: the warps that work share its issue slots, so it
-// looks at the clock only when it has not been woken.
+// Polls a barrier up to `tries` times, four instructions each.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint32_t tries) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 c;\n\tmov.u32 c, %3;\n\t"
+        "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "sub.u32 c, c, 1;\n\tsetp.ne.u32 q, c, 0;\n\t@q bra POLL;\n\t"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(tries)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait of a role.  The warps that work share its issue slots (longer
+// polls were most of what the kernel issued), so the clock and the abort flag
+// are looked at once in many polls.
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status,
                                           uint32_t site) {
-    if (mbar_try_wait(bar, parity)) return true;
-    uint64_t t0 = 0;
-    while (!mbar_try_wait_sleep(bar, parity)) {
+    if (mbar_poll(bar, parity, 4096)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_poll(bar, parity, 4096)) {
         if (*abort) return false;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
             report(status, BQ_ERR_TIMEOUT, site);
             *abort = 1;
             return false;
@@ -229,6 +241,12 @@ __device__ __forceinline__ void tmem_st_half<4>(uint32_t a, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld_half1(uint32_t a, uint32_t (&r)[2]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x1.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tmem_st_half1(uint32_t a, const uint32_t (&r)[2]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1, %2};" ::"r"(a), "r"(r[0]), "r"(r[1]) : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -246,14 +264,13 @@ __device__ __forceinline__ void regs_dec() {
 struct SeqWork {
     int64_t first;  // first row
     int64_t a0, step, cmax;
+    int64_t flat0, flat1;  // blocks that cost the least, blocks up to where all cost the most
     int64_t blocks;
     int64_t cost;  // of one head
     int rows, pos0, cap;
 };
 __device__ __forceinline__ int64_t cost_upto(const SeqWork &w, int64_t n) {
-    auto ceil_div = [](int64_t x, int64_t y) { return x <= 0 ? int64_t(0) : (x + y - 1) / y; };
-    const int64_t i1 = min(ceil_div(1 - w.a0, w.step), n);
-    const int64_t i2 = w.a0 > w.cmax ? i1 : max(i1, min((w.cmax - w.a0) / w.step + 1, n));
+    const int64_t i1 = min(w.flat0, n), i2 = max(i1, min(w.flat1, n));
     return n * kOverhead + i1 + (i2 - i1) * w.a0 + w.step * ((i1 + i2 - 1) * (i2 - i1) / 2) + (n - i2) * w.cmax;
 }
 __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int share) {
@@ -268,6 +285,11 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int sha
     w.a0 = w.pos0 + w.step;
     w.cmax = a.window > 0 ? a.window + w.step : int64_t(1) << 40;
     w.blocks = (static_cast<int64_t>(w.rows) * share + kCols - 1) / kCols;
+    // (step, share and the positions have 32 bits, and so have these quotients)
+    w.flat0 = w.a0 >= 1 ? 0 : static_cast<uint32_t>(w.step - w.a0) / static_cast<uint32_t>(w.step);
+    w.flat1 = w.a0 > w.cmax ? 0
+              : a.window > 0 ? static_cast<int64_t>(static_cast<uint32_t>(w.cmax - w.a0) / static_cast<uint32_t>(w.step)) + 1
+                             : w.blocks;
     w.cost = cost_upto(w, w.blocks);
     return w;
 }
@@ -286,8 +308,8 @@ struct Walk {
     int64_t at, stop, seq_begin;
     int b;
 };
-template <int TOK, int ALIGN>
-__device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, Walk &w, Segment &s, int64_t &end) {
+template <int TOK>
+__device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, int align, Walk &w, Segment &s, int64_t &end) {
     if (w.at >= w.stop) return false;
     SeqWork q = seq_work(a, w.b, share);
     while (w.at >= w.seq_begin + q.cost * a.pool.kv_heads) {
@@ -315,7 +337,7 @@ __device__ __forceinline__ bool next_segment(const Kv4AttnArgs &a, int share, Wa
     s.cap = q.cap;
     const int r0 = s.col0 / share, r1 = (s.col0 + s.ncols - 1) / share;
     const int64_t from = a.window > 0 ? max(static_cast<int64_t>(q.pos0) + r0 - a.window + 1, int64_t(0)) : 0;
-    s.start = static_cast<int>(from) & ~(ALIGN - 1);
+    s.start = static_cast<int>(from) & ~(align - 1);
     s.hi = static_cast<int>(min(static_cast<int64_t>(q.pos0) + r1, static_cast<int64_t>(q.cap) - 1));
     int tiles = 1;
     if (s.hi < static_cast<int>(from)) {
@@ -507,7 +529,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 k = min(k, 120);
                 const float up = !finite ? 0.0f : copysignf(__uint_as_float(static_cast<uint32_t>(127 + k) << 23), a.scale);
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                float f = fabsf(a.scale) * 1.4426950408889634f * down * 16777216.0f;  // codes are c 2^-24
+                // codes are c 2^-24; (not 0, so that what is hidden ends up far below what is seen)
+                float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * down * 16777216.0f, 7.8886090522101181e-31f);
                 if (MODS && a.softcap > 0.0f) f *= 2.0f / a.softcap;  // the argument of tanh, times 2 log2(e)
                 const uint32_t dst = base + C::OFF_Q + tile * C::QB + part * (D / 16) * (kRows * 16) + row * 16;
                 float sq = 0.0f;
@@ -571,7 +594,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 }
                 tc_fence_after();
                 const TileInfo info = s_info[buf];
-                const bool edge = tok0 + TOK - 1 > all_hi || tok0 < all_lo || info.odd != 0;
+                const bool edge = tok0 + TOK - 1 > all_hi || tok0 < all_lo;
                 const uint32_t par = base + C::OFF_P + buf * C::PB;
                 constexpr int NB = TOK / 8;
                 uint64_t y[NB][2];  // pairs of tokens 8 b + 2 t4, + 1 of row 8 i + g4
@@ -632,11 +655,14 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                     }
                 }
                 int see_lo[2], see_hi[2];  // first and last token that the row sees, from 2 t4 of the tile on
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    see_hi[i] = min(pos[i], g.hi) - tok0 - 2 * t4;
+                    see_lo[i] = a.window > 0 ? max(pos[i] - a.window + 1, 0) - tok0 - 2 * t4 : -TOK;
+                }
                 if (edge) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        see_hi[i] = min(pos[i], g.hi) - tok0 - 2 * t4;
-                        see_lo[i] = a.window > 0 ? max(pos[i] - a.window + 1, 0) - tok0 - 2 * t4 : -TOK;
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
                             float2 z = unpack64(y[b][i]);
@@ -706,9 +732,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                     for (int i = 0; i < 2; ++i) {
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            float2 x = unpack64(y[b][i]);
-                            if (edge && (8 * b > see_hi[i] || 8 * b < see_lo[i])) x.x = 0.0f;
-                            if (edge && (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i])) x.y = 0.0f;
+                            const float2 x = unpack64(y[b][i]);
                             sum[i] += x.x + x.y;
                         }
                     }
@@ -725,21 +749,27 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                             w[b][i] = pack_f16(x.x, x.y);
                         }
                     }
-                    if (edge) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                if (8 * b > see_hi[i] || 8 * b < see_lo[i]) w[b][i] &= 0xffff0000u;
-                                if (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i]) w[b][i] &= 0xffffu;
-                            }
-                        }
-                    }
 #pragma unroll
                     for (int b = 0; b + 4 <= NB; b += 4) tmem_st_half<4>(ts + r * (TOK / 2) + 4 * b, w[b]);
                     if constexpr (NB % 4 != 0) tmem_st_half<2>(ts + r * (TOK / 2) + 4 * (NB / 4 * 4), w[NB / 4 * 4]);
                 }
                 tmem_wait_st();
+                if (info.odd) {  // NaN for the rows that see such a token only (a weight of 0 times NaN is in its place)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < GR * NB; ++c0) {
+                        uint32_t w[2];
+                        tmem_ld_half1(ts + 4 * c0, w);
+                        tmem_wait_ld();
+                        const int b = c0 % NB;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (8 * b > see_hi[i] || 8 * b < see_lo[i]) w[i] &= 0xffff0000u;
+                            if (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i]) w[i] &= 0xffffu;
+                        }
+                        tmem_st_half1(ts + 4 * c0, w);
+                    }
+                    tmem_wait_st();
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(P_FULL + tile));
@@ -1061,8 +1091,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             walk.seq_begin = s_before;
             while (ok) {
                 int64_t end = 0;
-                const bool more = step == 16 ? next_segment<TOK, 16>(a, share, walk, g, end)
-                                             : next_segment<TOK, 32>(a, share, walk, g, end);
+                const bool more = next_segment<TOK>(a, share, step, walk, g, end);
                 if (!more) g.tiles = 0;
                 if (more && g.begins && !g.whole && lane == 0) {
                     const int64_t last = (end * ctas - 1) / total;  // CTA that holds the item's end
