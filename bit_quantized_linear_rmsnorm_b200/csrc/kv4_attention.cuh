@@ -124,7 +124,7 @@ template <int D, int G, int COLS, typename T>
 cudaError_t kv4_launch_join(const Kv4AttnArgs &a, const Kv4Ws &ws, unsigned grid, cudaStream_t s) {
     if (grid < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, COLS > 24 ? 8 : (COLS * D / 4 + kJoinThreads - 1) / kJoinThreads);
+    cfg.gridDim = dim3(grid - 1, COLS > 24 ? 32 : (COLS * D / 4 + kJoinThreads - 1) / kJoinThreads);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
             bool ok = true;
             // codes as fp16 subnormals, masked in place
             auto codes = [&](uint32_t src, uint32_t dst) {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < G / 32; ++i) {
                     // (the 16-byte pieces in an order that keeps 8 tokens off each other's banks)
                     const int ch = (i + (tok >> (C::ROW == 64 ? 1 : 2))) & (G / 32 - 1);
