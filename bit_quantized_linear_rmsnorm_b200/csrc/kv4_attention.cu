@@ -47,6 +47,7 @@ namespace {
 constexpr int kTile = 32;
 constexpr int kW = 8;  // warps
 constexpr int kThreads = kW * 32;
+constexpr int kStart = 8;  // cost of starting an item, in tiles
 constexpr float kSlack = 8.0f;      // a maximum is raised when passed by more
 constexpr float kFarStep = 0.001953125f;  // a step below 2^-9 of the largest is far from it
 
@@ -83,7 +84,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 // What the rows of sequence b need of the cache.
@@ -135,16 +136,16 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
     if (lane < C::S) mbar_init(bars + 8 * lane, 1);
     fence_mbarrier_init();
 
-    // ---- the share of this CTA: units [u, u_end) of the batch's list, a unit
-    // being a tile of one head and column block, tiles fastest, then column
-    // blocks, then heads, then sequences
+    // ---- the share of this CTA: units [u, u_end) of the batch's list, whose
+    // items (a head's column block of a sequence) count their tiles and
+    // kStart, column blocks fastest, then heads, then sequences
     const int64_t per = (a.seqs.batch + kThreads - 1) / kThreads;
     const int64_t b_lo = min(per * threadIdx.x, static_cast<int64_t>(a.seqs.batch));
     const int64_t b_hi = min(b_lo + per, static_cast<int64_t>(a.seqs.batch));
     int64_t mine = 0;
     for (int64_t b = b_lo; b < b_hi; ++b) {
         const SeqPlan p = plan_seq(a, static_cast<int>(b), share, C::COLS);
-        mine += static_cast<int64_t>(p.tiles) * p.blocks * a.pool.kv_heads;
+        mine += static_cast<int64_t>(p.tiles + kStart) * p.blocks * a.pool.kv_heads;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
     }
-    // a share is at least one tile per warp
+    // a share is at least about one tile per warp
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kW - 1) / kW);
     const int64_t cta = blockIdx.x;
     if (threadIdx.x == 0 && ws.desc != nullptr) ws.desc[cta].count = 0;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
         int64_t at = before;
         for (int64_t b = b_lo; b < b_hi; ++b) {
             const SeqPlan p = plan_seq(a, static_cast<int>(b), share, C::COLS);
-            const int64_t n = static_cast<int64_t>(p.tiles) * p.blocks * a.pool.kv_heads;
+            const int64_t n = static_cast<int64_t>(p.tiles + kStart) * p.blocks * a.pool.kv_heads;
             if (u_begin < at + n) {
                 s_b = static_cast<int>(b);
                 s_before = at;
@@ -188,16 +189,20 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
     for (int64_t u = u_begin; u < u_end;) {
         // ---- next segment: the part of one item that falls into the share
         SeqPlan p = plan_seq(a, b, share, C::COLS);
-        while (u >= seq_begin + static_cast<int64_t>(p.tiles) * p.blocks * a.pool.kv_heads) {
-            seq_begin += static_cast<int64_t>(p.tiles) * p.blocks * a.pool.kv_heads;
+        const auto cost = [&] { return static_cast<int64_t>(p.tiles + kStart) * p.blocks * a.pool.kv_heads; };
+        while (u >= seq_begin + cost()) {
+            seq_begin += cost();
             p = plan_seq(a, ++b, share, C::COLS);
         }
-        const int64_t item = (u - seq_begin) / p.tiles;
-        const int64_t item_begin = seq_begin + item * p.tiles, item_end = item_begin + p.tiles;
+        const int item_cost = p.tiles + kStart;
+        const int64_t item = (u - seq_begin) / item_cost;
+        const int64_t item_begin = seq_begin + item * item_cost, item_end = item_begin + item_cost;
         const int head = static_cast<int>(item / p.blocks), cb = static_cast<int>(item % p.blocks);
         const int64_t seg_end = min(item_end, u_end);
-        const int tile0 = p.t0 + static_cast<int>(u - item_begin);
-        const int ntiles = static_cast<int>(seg_end - u);
+        // (a part's tiles are in proportion to its cost; there may be none)
+        const int64_t first_tile = (u - item_begin) * p.tiles / item_cost;
+        const int tile0 = p.t0 + static_cast<int>(first_tile);
+        const int ntiles = static_cast<int>((seg_end - item_begin) * p.tiles / item_cost - first_tile);
         const int col0 = cb * C::COLS;  // columns: row of the sequence * share + head of the group
         const int ncols = min(C::COLS, p.rows * share - col0);
         const int64_t cap = min(static_cast<int64_t>(a.pool.table_width) << page_log2, int64_t(0x7fffffff));
@@ -227,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
         uint32_t bad_bits = 0;  // per stage, 2 bits: a half of the tile has no page
         auto issue = [&](int i) {
             const int stage = issued % C::S;
-            const int64_t s0 = __shfl_sync(0xffffffffu, src0, i & 31), s1 = __shfl_sync(0xffffffffu, src1, i & 31);
+            const int64_t s0 = __shfl_sync(0xffffffffu, src0, i & 31);
+            const int64_t s1 = page_log2 == 4 ? __shfl_sync(0xffffffffu, src1, i & 31) : -1;
             const uint32_t dst = ring + stage * C::STAGE, bar = bars + 8 * stage;
             const int parts = page_log2 == 4 ? 2 : 1;
             const int toks = kTile / parts;
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
         const int all_lo = a.window > 0 ? p.pos0 + row_hi - a.window + 1 : 0;
 
         float step_ref = 0.0f;  // about the largest value step so far
-        float o[NB][HV][4][4], m[NB][2], l[NB][2][GR], mo[NB][2][GR], lt[NB][2];
+        float o[NB][HV][4][4], m[NB][2], l[NB][2][GR], mo[NB][2][GR];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -373,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
                 m[nb][cc] = kNoMax;
-                lt[nb][cc] = 0.0f;
 #pragma unroll
                 for (int r = 0; r < GR; ++r) l[nb][cc][r] = mo[nb][cc][r] = 0.0f;
             }
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
 
             // ---- scores: z[block][nb][row half * 2 + column], in powers of two
             float z[2][NB][4];
-            float sv[2][2][GR], mv[2][2][GR];
+            float sv[2][2][GR], mv[2][2][GR], ri[2][2][GR];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float s[GR][NB][4];
@@ -440,17 +445,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                         const float2 y = unpack_f16(lds32(vp + tok * C::PAR + 4 * r));
                         sv[k][rh][r] = y.x;
                         mv[k][rh][r] = y.y;
-                    }
-                    if (edge) {
-                        const bool gone = (bad >> k) & 1u;
-#pragma unroll
-                        for (int r = 0; r < GR; ++r) {
-                            if (gone) ks[r] = __int_as_float(0x7fffffff);
-                            if (gone || tok0 + tok > p.hi) {  // a place that holds nothing
-                                sv[k][rh][r] = fmaxf(step_ref, 5.9604644775390625e-08f);
-                                mv[k][rh][r] = 0.0f;
-                            }
-                        }
+                        ri[k][rh][r] = rcp(y.x);
                     }
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
@@ -475,12 +470,29 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                             z[k][nb][2 * rh + cc] = x;
                         }
                     }
-                    if (edge) {
+                }
+            }
+            if (edge) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const bool gone = (bad >> k) & 1u;
+#pragma unroll
+                    for (int rh = 0; rh < 2; ++rh) {
+                        const int tok = 16 * k + gt + 8 * rh;
+                        if (gone || tok0 + tok > p.hi) {  // a place that holds nothing
+#pragma unroll
+                            for (int r = 0; r < GR; ++r) {
+                                sv[k][rh][r] = fmaxf(step_ref, 5.9604644775390625e-08f);
+                                mv[k][rh][r] = 0.0f;
+                                ri[k][rh][r] = rcp(sv[k][rh][r]);
+                            }
+                        }
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
                             for (int cc = 0; cc < 2; ++cc) {
                                 const int d = tok0 + tok - pos[nb][cc];
+                                if (gone) z[k][nb][2 * rh + cc] = __int_as_float(0x7fffffff);
                                 if (d > 0 || (a.window > 0 && d <= -a.window)) z[k][nb][2 * rh + cc] = -INFINITY;
                             }
                         }
@@ -492,56 +504,63 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
             // far below the others' would lose p * s_v to fp16's underflow, so such a token's weight goes into the
             // sums as it is (bits 2 (2 k + rh) + group)
             uint32_t direct = 0, spoilt = 0;
-            {
-                float lo = INFINITY, hi = 0.0f, odd = 0.0f;
+            float lv[2][2];  // log2 of the step, for the maximum
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int rh = 0; rh < 2; ++rh) {
+                    float x = sv[k][rh][0];
+                    if constexpr (GR == 2) x = fmaxf(x, sv[k][rh][1]);
+                    lv[k][rh] = lg2(x);
+                }
+            float lo = INFINITY, hi = 0.0f, odd = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int rh = 0; rh < 2; ++rh)
+#pragma unroll
+                    for (int r = 0; r < GR; ++r) {
+                        lo = fminf(lo, sv[k][rh][r]);
+                        hi = fmaxf(hi, sv[k][rh][r]);
+                        odd = fmaf(0.0f, sv[k][rh][r], fmaf(0.0f, mv[k][rh][r], odd));
+                    }
+            const bool care =
+                __any_sync(0xffffffffu, !(lo > step_ref * kFarStep && hi <= 2.0f * step_ref && odd == 0.0f));
+            if (care) {
+                hi = step_ref;
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int rh = 0; rh < 2; ++rh)
 #pragma unroll
                         for (int r = 0; r < GR; ++r) {
-                            lo = fminf(lo, sv[k][rh][r]);
-                            hi = fmaxf(hi, sv[k][rh][r]);
-                            odd = fmaf(0.0f, sv[k][rh][r], fmaf(0.0f, mv[k][rh][r], odd));
-                        }
-                if (__any_sync(0xffffffffu, !(lo > step_ref * kFarStep && hi <= 2.0f * step_ref && odd == 0.0f))) {
-                    hi = step_ref;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-                            for (int r = 0; r < GR; ++r) {
-                                if (!(fabsf(sv[k][rh][r]) <= 65504.0f && fabsf(mv[k][rh][r]) <= 65504.0f)) {
-                                    sv[k][rh][r] = mv[k][rh][r] = 0.0f;
-                                    spoilt |= 1u << (4 * k + 2 * rh + r);
-                                }
-                                hi = fmaxf(hi, sv[k][rh][r]);
+                            if (!(fabsf(sv[k][rh][r]) <= 65504.0f && fabsf(mv[k][rh][r]) <= 65504.0f)) {
+                                sv[k][rh][r] = mv[k][rh][r] = 0.0f;
+                                spoilt |= 1u << (4 * k + 2 * rh + r);
                             }
+                            hi = fmaxf(hi, sv[k][rh][r]);
+                        }
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                    step_ref = hi;
+                for (int o = 1; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+                step_ref = hi;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int rh = 0; rh < 2; ++rh)
+                    for (int rh = 0; rh < 2; ++rh) {
+                        float x = 5.9604644775390625e-08f;
 #pragma unroll
-                            for (int r = 0; r < GR; ++r)
-                                if (sv[k][rh][r] <= step_ref * kFarStep) direct |= 1u << (4 * k + 2 * rh + r);
-                }
+                        for (int r = 0; r < GR; ++r) {
+                            x = fmaxf(x, sv[k][rh][r]);
+                            if (sv[k][rh][r] <= step_ref * kFarStep) {
+                                direct |= 1u << (4 * k + 2 * rh + r);
+                                ri[k][rh][r] = 0.0f;  // (its share of the sums is added below)
+                            }
+                        }
+                        lv[k][rh] = lg2(x);
+                    }
             }
 
             // ---- running maximum of z + log2(step)
-            float lv[2][2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                for (int rh = 0; rh < 2; ++rh) {
-                    float x = sv[k][rh][0];
-                    if constexpr (GR == 2) x = fmaxf(x, sv[k][rh][1]);
-                    lv[k][rh] = lg2(fmaxf(x, 5.9604644775390625e-08f));
-                }
-            }
             bool rise = false;
             float top[NB][2];
 #pragma unroll
@@ -564,7 +583,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                         const float now = fmaxf(m[nb][cc], x);
                         const float keep = ex2(m[nb][cc] - now);
                         m[nb][cc] = now;
-                        lt[nb][cc] *= keep;
 #pragma unroll
                         for (int r = 0; r < GR; ++r) {
                             l[nb][cc][r] *= keep;
@@ -580,7 +598,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                     }
                 }
             }
-            const bool care = __any_sync(0xffffffffu, direct != 0);
 
             // ---- weights, and the products with the values
 #pragma unroll
@@ -588,36 +605,21 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                 uint32_t pb[NB][GR][2];  // weight * step, column g, tokens 2 t, 2 t + 1 (+ 8)
 #pragma unroll
                 for (int rh = 0; rh < 2; ++rh) {
-                    float ri[GR], zr[GR];
+                    float zr[GR];
 #pragma unroll
-                    for (int r = 0; r < GR; ++r) {
-                        ri[r] = (direct >> (4 * k + 2 * rh + r)) & 1u ? 0.0f : rcp(sv[k][rh][r]);
-                        zr[r] = mv[k][rh][r] * ri[r];
-                    }
+                    for (int r = 0; r < GR; ++r) zr[r] = mv[k][rh][r] * ri[k][rh][r];
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         const float e0 = ex2(z[k][nb][2 * rh] - (m[nb][0] - kLift));
                         const float e1 = ex2(z[k][nb][2 * rh + 1] - (m[nb][1] - kLift));
-                        lt[nb][0] += e0;
-                        lt[nb][1] += e1;
 #pragma unroll
                         for (int r = 0; r < GR; ++r) {
                             const uint32_t ph = pack_f16(e0 * sv[k][rh][r], e1 * sv[k][rh][r]);
                             const float2 w = unpack_f16(ph);
-                            l[nb][0][r] = fmaf(w.x, ri[r], l[nb][0][r]);
-                            l[nb][1][r] = fmaf(w.y, ri[r], l[nb][1][r]);
+                            l[nb][0][r] = fmaf(w.x, ri[k][rh][r], l[nb][0][r]);
+                            l[nb][1][r] = fmaf(w.y, ri[k][rh][r], l[nb][1][r]);
                             mo[nb][0][r] = fmaf(w.x, zr[r], mo[nb][0][r]);
                             mo[nb][1][r] = fmaf(w.y, zr[r], mo[nb][1][r]);
-                            if (care && ((direct >> (4 * k + 2 * rh + r)) & 1u)) {
-                                l[nb][0][r] += e0;
-                                l[nb][1][r] += e1;
-                                mo[nb][0][r] = fmaf(e0, mv[k][rh][r], mo[nb][0][r]);
-                                mo[nb][1][r] = fmaf(e1, mv[k][rh][r], mo[nb][1][r]);
-                                if ((spoilt >> (4 * k + 2 * rh + r)) & 1u) {  // NaN for the rows that see it
-                                    if (z[k][nb][2 * rh] > -INFINITY) mo[nb][0][r] = __int_as_float(0x7fffffff);
-                                    if (z[k][nb][2 * rh + 1] > -INFINITY) mo[nb][1][r] = __int_as_float(0x7fffffff);
-                                }
-                            }
                             pb[nb][r][rh] = transpose8x8(ph);
                         }
                     }
@@ -639,6 +641,27 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                     }
                 }
             }
+            if (care) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int rh = 0; rh < 2; ++rh)
+#pragma unroll
+                        for (int r = 0; r < GR; ++r) {
+                            if (!((direct >> (4 * k + 2 * rh + r)) & 1u)) continue;
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int cc = 0; cc < 2; ++cc) {
+                                    const float x = z[k][nb][2 * rh + cc], e = ex2(x - (m[nb][cc] - kLift));
+                                    l[nb][cc][r] += e;
+                                    mo[nb][cc][r] = fmaf(e, mv[k][rh][r], mo[nb][cc][r]);
+                                    // NaN for the rows that see it
+                                    if (((spoilt >> (4 * k + 2 * rh + r)) & 1u) && x > -INFINITY)
+                                        mo[nb][cc][r] = __int_as_float(0x7fffffff);
+                                }
+                        }
+            }
             ++taken;
             __syncwarp();
             if (next < mytiles) {
@@ -655,7 +678,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
             for (int cc = 0; cc < 2; ++cc) {
 #pragma unroll
                 for (int s = 4; s < 32; s <<= 1) {
-                    lt[nb][cc] += __shfl_xor_sync(0xffffffffu, lt[nb][cc], s);
 #pragma unroll
                     for (int r = 0; r < GR; ++r) {
                         l[nb][cc][r] += __shfl_xor_sync(0xffffffffu, l[nb][cc][r], s);
@@ -690,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                     }
                     if (g == 0) {
                         aux[c] = m[nb][cc];
-                        aux[C::COLS + c] = lt[nb][cc];
+                        aux[C::COLS + c] = l[nb][cc][0];
 #pragma unroll
                         for (int r = 0; r < GR; ++r) aux[(2 + r) * C::COLS + c] = l[nb][cc][r];
                     }

@@ -107,12 +107,6 @@ __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatil
     }
     return true;
 }
-__device__ __forceinline__ bool elect_one() {  // one lane of a converged warp
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // A row of the tiles, for the lanes that hold its scores; then what they found.
 struct RowInfo {
     float f, sq[2], slope;
