@@ -465,50 +465,51 @@ def bq_kv4_page_bytes(page_size: int, head_dim: int, group_size: int) -> int:
 
 
 def _kv4_cache(cache: torch.Tensor, D: int, group_size: int, *tables):
-    """(pages, page stride, page size, heads) of a cache [pages, kv_heads, page_bytes], after checking it and the
-    int32 tables that go with it (None: not given)."""
-    if cache.dtype != torch.uint8 or cache.dim() != 3 or group_size < 1 or D % group_size != 0:
+    """(pages, page stride, page size, kv_heads) of a cache, after checking it and the integer tables that go with it.
+
+    (A decode step is a few microseconds long, so these checks ask a tensor for as little as they can.)"""
+    if cache.dtype is not torch.uint8 or cache.dim() != 3 or group_size < 1 or D % group_size != 0:
         raise ValueError("expected a uint8 cache [pages, kv_heads, page_bytes] and a group_size that divides head_dim")
     pages, H, nbytes = cache.shape
-    page = nbytes // (D + 8 * (D // group_size))
-    if page * (D + 8 * (D // group_size)) != nbytes or (pages and (cache.stride(2) != 1 or
-                                                                   (H > 1 and cache.stride(1) != nbytes))):
+    pstride, hstride, inner = cache.stride()
+    token = D + 8 * (D // group_size)
+    page = nbytes // token
+    if page * token != nbytes or (pages and (inner != 1 or (H > 1 and hstride != nbytes))):
         raise ValueError("the cache's last two dimensions must be dense, of bq_kv4_page_bytes() bytes per head")
+    dev = cache.get_device()
+    if dev < 0:
+        raise ValueError("the cache must be on a GPU")
     for t in tables:
-        if t is not None and (t.dtype != torch.int32 or t.device != cache.device or
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev or
                               (t.stride(-1) != 1 and t.shape[-1] > 1)):
             raise ValueError("block_table, lengths and offsets must be int32 on the cache's device, dense along a row")
-    return pages, (cache.stride(0) if pages > 1 else H * nbytes), page, H
-
-
-def _kv4_ld(table: torch.Tensor) -> int:
-    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+    return pages, (pstride if pages > 1 else H * nbytes), page, H
 
 
 def _kv4_batch(block_table, lens, cu, starts=None):
-    """Number of sequences, after checking that the tables agree on it."""
+    """(sequences, row stride, width) of a block table, after checking that the tables agree on the first."""
     if block_table.dim() != 2:
         raise ValueError("expected a block_table [batch, pages of a sequence]")
-    B = block_table.shape[0]
+    B, width = block_table.shape
     if (lens is not None and lens.shape != (B,)) or (cu is not None and cu.shape != (B + 1,)) or \
             (starts is not None and starts.shape != (B,)):
         raise ValueError("lengths [batch] and offsets [batch + 1] must match block_table [batch, ...]")
-    return B
+    return B, (block_table.stride(0) if B > 1 else width), width
 
 
-def _step(t: torch.Tensor, dim: int) -> int:
-    """Stride of a dimension that is walked along (that of a dimension of one element is anything)."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+def _kv4_strides(t: torch.Tensor):
+    """Token and head strides of [T, heads, D] (0 for a dimension of one element, whose stride is anything)."""
+    st, sh, _ = t.stride()
+    T, H, _ = t.shape
+    return (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
-def _kv4_call(device, call, stream):
-    """call(stream handle) with `device` current (the library launches on the current device)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        return call(s.cuda_stream)
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream() if stream is None else stream
-        return call(s.cuda_stream)
+def _kv4_call(dev: int, fn, stream, *args):
+    """fn(*args, stream handle) with device `dev` current (the library launches on the current device)."""
+    if dev == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
 def bq_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -516,18 +517,20 @@ def bq_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_ta
     """Quantizes new key and value rows [T, kv_heads, D] into their pages of `cache` (uint8 [pages, kv_heads,
     page_bytes]); returns the cache.  seq_lens counts the rows written; cu_q [batch + 1] gives the rows of each
     sequence (None: T / batch each)."""
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.device != cache.device or \
-            v.device != cache.device or (k.numel() and (k.stride(2) != 1 or v.stride(2) != 1)):
+    dev = cache.get_device()
+    if k.dim() != 3 or k.shape != v.shape or k.dtype is not v.dtype or k.get_device() != dev or \
+            v.get_device() != dev or (k.numel() and (k.stride(2) != 1 or v.stride(2) != 1)):
         raise ValueError("expected k and v [T, kv_heads, D] of one type, dense along D, on the cache's device")
     T, H, D = k.shape
     pages, pstride, page, Hc = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
     if H != Hc or k.dtype not in _DTYPE:
         raise ValueError("k and v must have the cache's heads and a supported type")
-    B = _kv4_batch(block_table, seq_lens, cu_q)
-    st = _kv4_call(cache.device, lambda s: lib().bq_kv4_write(
-        k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], T, H, D, _step(k, 0), _step(k, 1), _step(v, 0), _step(v, 1),
-        None if cu_q is None else cu_q.data_ptr(), seq_lens.data_ptr(), B, block_table.data_ptr(),
-        _kv4_ld(block_table), block_table.shape[1], cache.data_ptr(), pages, pstride, page, group_size, s), stream)
+    B, ld, width = _kv4_batch(block_table, seq_lens, cu_q)
+    kt, kh = _kv4_strides(k)
+    vt, vh = _kv4_strides(v)
+    st = _kv4_call(dev, lib().bq_kv4_write, stream, k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], T, H, D, kt, kh, vt, vh,
+                   None if cu_q is None else cu_q.data_ptr(), seq_lens.data_ptr(), B, block_table.data_ptr(), ld, width,
+                   cache.data_ptr(), pages, pstride, page, group_size)
     _check(st, "bq_kv4_write")
     return cache
 
@@ -537,19 +540,18 @@ def bq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Te
     """(k, v) [total, kv_heads, D]: positions starts[b] + j (starts None: 0) of each sequence, its rows cu_len[b] up
     to cu_len[b + 1]."""
     pages, pstride, page, H = _kv4_cache(cache, head_dim, group_size, block_table, cu_len, starts)
-    B = _kv4_batch(block_table, None, cu_len, starts)
-    shape = (total, H, head_dim)
+    B, ld, width = _kv4_batch(block_table, None, cu_len, starts)
+    shape, dev = (total, H, head_dim), cache.get_device()
     if k is None:
         k = torch.empty(shape, dtype=out_dtype, device=cache.device)
     if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
-    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.dtype not in _DTYPE or \
-            not (k.is_contiguous() and v.is_contiguous()) or k.device != cache.device or v.device != cache.device:
+        v = torch.empty_like(k)
+    if k.shape != shape or v.shape != shape or k.dtype is not v.dtype or k.dtype not in _DTYPE or \
+            not (k.is_contiguous() and v.is_contiguous()) or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("k and v must be dense [total, kv_heads, head_dim] of one type on the cache's device")
-    st = _kv4_call(cache.device, lambda s: lib().bq_kv4_read(
-        cache.data_ptr(), pages, pstride, page, H, head_dim, group_size, block_table.data_ptr(), _kv4_ld(block_table),
-        block_table.shape[1], None if starts is None else starts.data_ptr(), cu_len.data_ptr(), B, total,
-        _DTYPE[k.dtype], k.data_ptr(), v.data_ptr(), s), stream)
+    st = _kv4_call(dev, lib().bq_kv4_read, stream, cache.data_ptr(), pages, pstride, page, H, head_dim, group_size,
+                   block_table.data_ptr(), ld, width, None if starts is None else starts.data_ptr(), cu_len.data_ptr(),
+                   B, total, _DTYPE[k.dtype], k.data_ptr(), v.data_ptr())
     _check(st, "bq_kv4_read")
     return k, v
 
@@ -564,31 +566,31 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
     """Causal attention of q [T, q_heads, D] over a 4-bit cache: each sequence's rows stand at the end of its
     seq_lens tokens.  cu_q [batch + 1] gives the rows of each sequence (None: T / batch each), max_q the most rows of
     one (None: T).  Returns out [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given."""
-    if q.dim() != 3 or q.device != cache.device or q.dtype not in _DTYPE or (q.numel() and q.stride(2) != 1):
+    dev = cache.get_device()
+    if q.dim() != 3 or q.get_device() != dev or q.dtype not in _DTYPE or (q.numel() and q.stride(2) != 1):
         raise ValueError("expected q [T, q_heads, D], dense along D, on the cache's device")
     T, Hq, D = q.shape
     pages, pstride, page, H = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
-    B = _kv4_batch(block_table, seq_lens, cu_q)
+    B, ld, width = _kv4_batch(block_table, seq_lens, cu_q)
     if out is None:
         out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+    elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be dense, of q's shape, type and device")
-    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (Hq,) or slopes.device != q.device or
-                               not slopes.is_contiguous()):
+    if slopes is not None and (slopes.dtype is not torch.float32 or slopes.shape != (Hq,) or
+                               slopes.get_device() != dev or not slopes.is_contiguous()):
         raise ValueError("slopes must be dense fp32 [q_heads] on q's device")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or lse.device != q.device or
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or lse.get_device() != dev or
                             not lse.is_contiguous()):
         raise ValueError("lse must be dense fp32 [T, q_heads] on q's device")
     if workspace is None:
         workspace = torch.empty(bq_kv4_attention_workspace_bytes(T, Hq, H, D), dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be dense and on q's device")
-    st = _kv4_call(cache.device, lambda s: lib().bq_kv4_attention(
-        q.data_ptr(), _DTYPE[q.dtype], T, Hq, D, _step(q, 0), _step(q, 1), None if cu_q is None else cu_q.data_ptr(),
-        T if max_q is None else max_q, seq_lens.data_ptr(), B, block_table.data_ptr(), _kv4_ld(block_table),
-        block_table.shape[1], cache.data_ptr(), pages, pstride, page, H, group_size,
-        D ** -0.5 if scale is None else scale, window, softcap, None if slopes is None else slopes.data_ptr(),
-        out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), s), stream)
+    qt, qh = _kv4_strides(q)
+    st = _kv4_call(dev, lib().bq_kv4_attention, stream, q.data_ptr(), _DTYPE[q.dtype], T, Hq, D, qt, qh,
+                   None if cu_q is None else cu_q.data_ptr(), T if max_q is None else max_q, seq_lens.data_ptr(), B,
+                   block_table.data_ptr(), ld, width, cache.data_ptr(), pages, pstride, page, H, group_size,
+                   D ** -0.5 if scale is None else scale, window, softcap, None if slopes is None else slopes.data_ptr(),
+                   out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     _check(st, "bq_kv4_attention")
     return out

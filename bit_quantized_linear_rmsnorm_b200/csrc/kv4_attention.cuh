@@ -3,6 +3,8 @@
 // them.
 #pragma once
 
+#include <algorithm>
+
 #include "kv4_common.cuh"
 
 namespace bq {
@@ -77,45 +79,85 @@ inline Kv4Ws kv4_workspace(void *ws) {
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWays = 8;  // threads that share the partial results of four dims
 
+// Every load of a partial result is independent of the others (no branch
+// between them), and kJoinWays threads take every kJoinWays-th one: what bounds
+// this kernel is the latency of a few dependent steps.
 template <int D, int G, int COLS, typename T>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArgs a, const Kv4Ws ws) {
     constexpr int64_t SLOT = static_cast<int64_t>(COLS) * (D + 4);
+    constexpr int PER = kJoinThreads / kJoinWays;  // groups of four dims of a block, one way each
+    __shared__ float4 s_num[kJoinWays][PER];
+    __shared__ float s_top[kJoinWays][PER], s_den[kJoinWays][PER], s_sum[kJoinWays][PER];
     pdl_wait();
     const int64_t cta = blockIdx.x;
     const Kv4Partial it = ws.desc[cta];
     if (it.count <= 1) return;
     const int share = a.q_heads / a.pool.kv_heads;
-    for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < it.cols * (D / 4); e += gridDim.y * kJoinThreads) {
-        const int c = e / (D / 4), d = e % (D / 4) * 4;
-        const float *s0 = ws.slots + (2 * cta + 1) * SLOT + c * (D + 4);
-        const float *s1 = ws.slots + 2 * (cta + 1) * SLOT + c * (D + 4);  // then 2 slots on
-        float top = s0[D];
+    const int way = threadIdx.x / PER, mine = threadIdx.x % PER;
+    for (int e0 = blockIdx.y * PER; e0 < it.cols * (D / 4); e0 += gridDim.y * PER) {
+        const int e = e0 + mine;  // (D / 4 is a multiple of 16, but a block may reach past the last column)
+        const bool on = e < it.cols * (D / 4);
+        const int c = on ? e / (D / 4) : 0, d = e % (D / 4) * 4;
+        // slot 2 cta + 1 first, then every second one
+        const float *s0 = ws.slots + 2 * cta * SLOT + c * (D + 4);
+        auto part = [&](int i) { return s0 + (i == 0 ? SLOT : 2 * i * SLOT); };
+        float top = kNoMax;
 #pragma unroll 8
-        for (int i = 1; i < it.count; ++i) top = fmaxf(top, s1[(i - 1) * 2 * SLOT + D]);
+        for (int i = way; i < it.count; i += kJoinWays) top = fmaxf(top, part(i)[D]);
         float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float den = 0.0f, sum = 0.0f;
 #pragma unroll 4
-        for (int i = 0; i < it.count; ++i) {
-            const float *s = i == 0 ? s0 : s1 + (i - 1) * 2 * SLOT;
-            const float m = s[D];
-            if (s[D + 1] == 0.0f) continue;
-            const float k = ex2(m - top);
-            const float4 v = *reinterpret_cast<const float4 *>(s + d);
+        for (int i = way; i < it.count; i += kJoinWays) {
+            const float *s = part(i);
+            float4 v = *reinterpret_cast<const float4 *>(s + d);
+            const float4 st = *reinterpret_cast<const float4 *>(s + D);  // maximum, sum, divisors
+            float ds = d < G ? st.z : st.w;
+            const bool none = st.y == 0.0f;  // (the rest of the slot may never have been written)
+            const float k = none ? 0.0f : ex2(st.x - top);
+            if (none) {
+                v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                ds = 0.0f;
+            }
             num.x = fmaf(v.x, k, num.x);
             num.y = fmaf(v.y, k, num.y);
             num.z = fmaf(v.z, k, num.z);
             num.w = fmaf(v.w, k, num.w);
-            den = fmaf(s[D + 2 + d / G], k, den);
-            sum = fmaf(s[D + 1], k, sum);
+            den = fmaf(ds, k, den);
+            sum = fmaf(st.y, k, sum);
         }
-        const int col = it.col0 + c, row = col / share, hh = col - row * share;
-        const int64_t to = (it.first + row) * a.q_heads + static_cast<int64_t>(it.head) * share + hh;
-        const float inv = den == 0.0f ? 0.0f : __fdividef(1.0f, den);
-        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + to * D + d) =
-            make_uint2(pack2(num.x * inv, num.y * inv, T()), pack2(num.z * inv, num.w * inv, T()));
-        if (a.lse != nullptr && d == 0)
-            a.lse[to] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
+        s_num[way][mine] = num;
+        s_top[way][mine] = top;
+        s_den[way][mine] = den;
+        s_sum[way][mine] = sum;
+        __syncthreads();
+        if (way == 0 && on) {
+            top = s_top[0][mine];
+#pragma unroll
+            for (int w = 1; w < kJoinWays; ++w) top = fmaxf(top, s_top[w][mine]);
+            num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            den = sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWays; ++w) {
+                const float k = ex2(s_top[w][mine] - top);
+                const float4 v = s_num[w][mine];
+                num.x = fmaf(v.x, k, num.x);
+                num.y = fmaf(v.y, k, num.y);
+                num.z = fmaf(v.z, k, num.z);
+                num.w = fmaf(v.w, k, num.w);
+                den = fmaf(s_den[w][mine], k, den);
+                sum = fmaf(s_sum[w][mine], k, sum);
+            }
+            const int col = it.col0 + c, row = col / share, hh = col - row * share;
+            const int64_t to = (it.first + row) * a.q_heads + static_cast<int64_t>(it.head) * share + hh;
+            const float inv = den == 0.0f ? 0.0f : __fdividef(1.0f, den);
+            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + to * D + d) =
+                make_uint2(pack2(num.x * inv, num.y * inv, T()), pack2(num.z * inv, num.w * inv, T()));
+            if (a.lse != nullptr && d == 0)
+                a.lse[to] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
+        }
+        __syncthreads();
     }
 }
 
@@ -124,7 +166,7 @@ template <int D, int G, int COLS, typename T>
 cudaError_t kv4_launch_join(const Kv4AttnArgs &a, const Kv4Ws &ws, unsigned grid, cudaStream_t s) {
     if (grid < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, COLS > 24 ? 32 : (COLS * D / 4 + kJoinThreads - 1) / kJoinThreads);
+    cfg.gridDim = dim3(grid - 1, std::min(COLS * D / 4 * kJoinWays / kJoinThreads, 32));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
