@@ -45,9 +45,9 @@ namespace bq {
 namespace {
 
 constexpr int kTile = 32;
-constexpr int kW = 8;  // warps
+constexpr int kW = 4;  // warps
 constexpr int kThreads = kW * 32;
-constexpr int kStart = 8;  // cost of starting an item, in tiles
+constexpr int kStart = 6;  // cost of starting an item, in tiles
 constexpr float kSlack = 8.0f;      // a maximum is raised when passed by more
 constexpr float kFarStep = 0.001953125f;  // a step below 2^-9 of the largest is far from it
 
@@ -61,8 +61,8 @@ struct Shape {
     static constexpr int PAR = 4 * GR;           // bytes of parameters of a token
     static constexpr int CODES = kTile * ROW, PARS = kTile * PAR;
     static constexpr int STAGE = 2 * (CODES + PARS);
-    static constexpr int CTAS = NB == 1 ? 2 : 1;  // per SM
-    static constexpr int S = 3 * (NB == 1 ? 1 : 2);  // stages of a warp
+    static constexpr int CTAS = NB == 1 ? 3 : 2;  // per SM
+    static constexpr int S = NB == 1 ? 4 : 5;  // stages of a warp
     static constexpr int COLS = 8 * NB;
     static constexpr int CSTR = D + 8;  // floats between columns of a warp's results
     static constexpr int RES = (COLS * CSTR + COLS * (2 + GR)) * 4;  // bytes of a warp's results
@@ -795,9 +795,9 @@ cudaError_t launch_decode(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &d
 }  // namespace
 
 size_t kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
-    // slots of a CTA: 2, for one CTA per SM with 24 columns, or two with 8; many rows: one with 256
-    const int64_t cols = total * (q_heads / kv_heads) > kKv4FewColumns ? 256 : 24;
-    return 2 * kKv4MaxSms * (sizeof(Kv4Partial) + static_cast<size_t>(cols * (head_dim + 4)) * 4);
+    // two slots for each CTA: three per SM with 8 columns, two with 24, or, for many rows, one with 256
+    const int64_t cols = total * (q_heads / kv_heads) > kKv4FewColumns ? 256 : 48;
+    return kKv4MaxCtas * sizeof(Kv4Partial) + 2 * kKv4MaxSms * static_cast<size_t>(cols * (head_dim + 4)) * 4;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {

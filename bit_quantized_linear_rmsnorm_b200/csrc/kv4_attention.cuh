@@ -11,6 +11,7 @@ namespace bq {
 namespace {
 
 constexpr int kKv4MaxSms = 160;
+constexpr int kKv4MaxCtas = 3 * kKv4MaxSms;
 constexpr float kNoMax = -3.0e38f;  // running maximum (in powers of two) before any token
 constexpr float kLift = 7.0f;       // weights are 2^(z - maximum + kLift)
 
@@ -75,18 +76,20 @@ struct Kv4Ws {
 };
 inline Kv4Ws kv4_workspace(void *ws) {
     return {static_cast<Kv4Partial *>(ws),
-            reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 2 * kKv4MaxSms * sizeof(Kv4Partial))};
+            reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kKv4MaxCtas * sizeof(Kv4Partial))};
 }
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinWays = 8;  // threads that share the partial results of four dims
+// Threads that share the partial results of four dims: few rows are split over many CTAs, many rows over two or three.
+constexpr int join_ways(int cols) { return cols > 24 ? 1 : 8; }
 
 // Every load of a partial result is independent of the others (no branch
-// between them), and kJoinWays threads take every kJoinWays-th one: what bounds
+// between them), and join_ways threads take every so many-th one: what bounds
 // this kernel is the latency of a few dependent steps.
 template <int D, int G, int COLS, typename T>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArgs a, const Kv4Ws ws) {
     constexpr int64_t SLOT = static_cast<int64_t>(COLS) * (D + 4);
+    constexpr int kJoinWays = join_ways(COLS);
     constexpr int PER = kJoinThreads / kJoinWays;  // groups of four dims of a block, one way each
     __shared__ float4 s_num[kJoinWays][PER];
     __shared__ float s_top[kJoinWays][PER], s_den[kJoinWays][PER], s_sum[kJoinWays][PER];
@@ -166,7 +169,7 @@ template <int D, int G, int COLS, typename T>
 cudaError_t kv4_launch_join(const Kv4AttnArgs &a, const Kv4Ws &ws, unsigned grid, cudaStream_t s) {
     if (grid < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, std::min(COLS * D / 4 * kJoinWays / kJoinThreads, 32));
+    cfg.gridDim = dim3(grid - 1, std::min(COLS * D / 4 * join_ways(COLS) / kJoinThreads, 32));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
