@@ -42,20 +42,6 @@ __device__ __forceinline__ void kv4_rows(const Kv4Seqs &s, int b, int64_t &first
     }
 }
 
-// Block of the page that holds position `pos` of sequence b, or nullptr (and
-// the status word set) where the table has no page of the pool there.
-__device__ __forceinline__ uint8_t *kv4_block(const Kv4Pool &p, int b, int pos, int head, uint32_t *status,
-                                              uint32_t site) {
-    const int i = pos >> p.page_log2;
-    int page = -1;
-    if (i < p.table_width) page = __ldg(p.table + static_cast<int64_t>(b) * p.table_ld + i);
-    if (page < 0 || page >= p.pages) {
-        report(status, BQ_ERR_INVALID_ARG, site);
-        return nullptr;
-    }
-    return p.pool + static_cast<int64_t>(page) * p.page_stride + static_cast<int64_t>(head) * p.block_bytes;
-}
-
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -124,12 +110,22 @@ struct Kv4In<__half> {
     }
 };
 
-// What code j (0..7) of a word stands for: step * code + minimum.  The code
-// is exact in fp32 (as 2^23 + code, less 2^23), its product with the step
-// (4 x 11 bits) too, so the sum is the only rounding.
-__device__ __forceinline__ float kv4_value(uint32_t word, int j, float step, float minimum) {
-    const float c = __uint_as_float(((word >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.0f;
-    return fmaf(c, step, minimum);
+// What the eight codes of a word stand for: step * code + minimum.  A code
+// masked in place is an fp16 subnormal, code * 2^-24 or (the upper half of a
+// byte) code * 2^-20; times the step with that power of two in it (4 x 11 bits)
+// it is exact in fp32, so the sum is the only rounding.
+__device__ __forceinline__ void kv4_values(uint32_t word, float2 step_minimum, float (&f)[8]) {
+    const float s0 = step_minimum.x * 16777216.0f, s1 = step_minimum.x * 1048576.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t w = word >> (8 * j), lo = w & 0x000f000fu, hi = w & 0x00f000f0u;
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));  // elements 2 j, 2 j + 4
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));  // 2 j + 1, 2 j + 5
+        f[2 * j] = fmaf(a.x, s0, step_minimum.y);
+        f[2 * j + 4] = fmaf(a.y, s0, step_minimum.y);
+        f[2 * j + 1] = fmaf(b.x, s1, step_minimum.y);
+        f[2 * j + 5] = fmaf(b.y, s1, step_minimum.y);
+    }
 }
 
 }  // namespace bq
