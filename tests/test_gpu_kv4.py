@@ -414,3 +414,119 @@ def test_prompt_then_captured_decoding(D, G, page):
         assert np.array_equal(pool.cpu().numpy(), s.host.pool)
         check_attention(s, out, None, q, one, D ** -0.5)
     status_ok()
+
+
+# ------------------------------------------------------------------ many rows: steps of every size, parts, head layouts
+def steps_cache(kind, D, G, n, H=1, page=32, seed=12):
+    """A sequence whose value groups differ in a way that the many-row kernel has to follow."""
+    s = Setup([n], H, D, G, page, seed=seed)
+    for p in range(n):
+        k, v = s.rng.standard_normal((2, H, D)).astype(np.float32)
+        if kind == "growing":  # each 50 tokens a hundred times larger, and their minima
+            v = v * 10.0 ** (2 * (p // 50) - 4)
+        elif kind == "shrinking":
+            v = v * 10.0 ** (4 - 2 * (p // 50))
+        elif kind == "mixed":  # orders of magnitude side by side, and constant groups
+            v = v * 10.0 ** -(p % 5) if p % 7 else np.full_like(v, 2.5)
+        elif kind == "zero":
+            v = np.zeros_like(v)
+        elif kind == "offset":  # far from zero: the minimum outweighs the step
+            v = v * 0.01 + (40 if p % 2 else -3000)
+        elif kind == "tiny":
+            v = v * 2.0 ** -16
+        s.host.put(*s.place(0, p), k, np.clip(v, -6.5e4, 6.5e4).astype(np.float32))
+    return s
+
+
+@pytest.mark.parametrize("kind", ["growing", "shrinking", "mixed", "zero", "offset", "tiny"])
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_value_steps_of_every_size(kind, D, G):
+    s = steps_cache(kind, D, G, 260)
+    run_attention(s, query(s, 100, 2, "f16"), [100])
+    run_attention(s, query(s, 100, 2, "bf16", scale=6.0), [100])  # few tokens carry most of the weight
+    run_attention(s, query(s, 1, 2, "f16"), [1])
+
+
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_weights_that_rise_late(D, G):
+    """Scores that grow along the sequence, so that the running maximum is passed by a lot inside a tile and between tiles,
+    with rows that begin to see tokens in the middle of one."""
+    s = Setup([400], 1, D, G, 64, seed=13)
+    for p in range(400):
+        k, v = s.rng.standard_normal((2, 1, D)).astype(np.float32)
+        s.host.put(*s.place(0, p), k + (p // 20) * 0.5, v)
+    q = (torch.ones(90, 4, D) + 0.1 * torch.from_numpy(s.rng.standard_normal((90, 4, D)))).to(torch.bfloat16).cuda()
+    for kw in (dict(), dict(window=70), dict(slopes=np.array([0.5, 0.1, 0.0, 2.0])), dict(softcap=30.0)):
+        run_attention(s, q, [90], **kw)
+        run_attention(s, q[:1], [1], **kw)
+
+
+@pytest.mark.parametrize("share", [1, 3, 5, 12, 40, 300])
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 64)])
+def test_any_number_of_heads_to_a_key_head(share, D, G):
+    """Rows and heads fill column blocks that begin and end inside a row, in one tile of rows or two."""
+    s = Setup([75, 0, 40], 2, D, G, 16, seed=14).fill()
+    counts = [9, 3, 30]
+    run_attention(s, query(s, sum(counts) + 2, 2 * share, "bf16"), counts, rows_behind=2)
+
+
+def test_items_cut_between_ctas():
+    """Few columns and many tokens: every item is cut into parts, with column blocks of one tile of rows and of two."""
+    s = Setup([3000, 130, 1700], 1, 64, 64, 128, seed=15).fill()
+    for counts, Hq in (([40, 5, 90], 1), ([90, 0, 33], 4)):
+        run_attention(s, query(s, sum(counts), Hq, "f16"), counts)
+        run_attention(s, query(s, sum(counts), Hq, "bf16"), counts, window=1000, softcap=20.0)
+
+
+def test_many_rows_captured_and_replayed():
+    """One graph of a chunk, replayed with other lengths, offsets and pages; two graphs that share a workspace."""
+    H, Hq, D, G, page = 2, 6, 128, 128, 32
+    s = Setup([300, 200], H, D, G, page, seed=16).fill()
+    pool, table, lens, cu = s.cuda(), dev(s.table), dev([300, 200]), dev([0, 60, 100])
+    q = query(s, 100, Hq, "bf16")
+    out = torch.full_like(q, 3.0)
+    ws = torch.empty(bq.bq_kv4_attention_workspace_bytes(100, Hq, H, D), dtype=torch.uint8, device="cuda")
+
+    def call():
+        bq.bq_kv4_attention(q, pool, table, lens, G, cu_q=cu, max_q=100, out=out, workspace=ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            call()
+    for i, (ln, off) in enumerate(([[300, 200], [0, 60, 100]], [[100, 64], [0, 1, 41]], [[31, 0], [0, 31, 31]],
+                                   [[299, 200], [0, 0, 100]])):
+        s.lens = ln
+        lens.copy_(dev(ln))
+        cu.copy_(dev(off))
+        out.fill_(3.0)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        check_attention(s, out, None, q, off, D ** -0.5)
+        assert (out[off[-1]:] == 3).all()
+    status_ok()
+
+
+def test_wrappers_refuse_what_is_not_on_the_device():
+    s = Setup([20], 2, 64, 64, 16, seed=17).fill()
+    pool, table, lens = s.cuda(), dev(s.table), dev(s.lens)
+    q = query(s, 1, 4, "bf16")
+    kv = torch.randn(1, 2, 64, device="cuda").bfloat16()
+    for bad in (dict(q=q.cpu()), dict(q=q.float().double()), dict(table=table.cpu()), dict(table=table.long()),
+                dict(lens=lens.cpu()), dict(pool=pool.cpu()), dict(pool=pool[..., :-1])):
+        a = dict(q=q, pool=pool, table=table, lens=lens)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            bq.bq_kv4_attention(a["q"], a["pool"], a["table"], a["lens"], 64)
+        if "q" not in bad:
+            with pytest.raises(ValueError):
+                bq.bq_kv4_write(kv, kv, a["pool"], a["table"], a["lens"], 64)
+    with pytest.raises(ValueError):
+        bq.bq_kv4_write(kv, kv.cpu(), pool, table, lens, 64)
+    with pytest.raises(ValueError):
+        bq.bq_kv4_read(pool, table, dev([0, 20]).cpu(), 20, 64, 64)
+    status_ok()
