@@ -82,6 +82,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Codes less 8, both as pairs of fp16 subnormals: exact.
+__device__ __forceinline__ uint32_t from_middle(uint32_t codes, uint32_t eight) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(codes), "r"(eight));
+    return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                         km[r] = x.y;
                         const float2 y = unpack_f16(lds32(vp + tok * C::PAR + 4 * r));
                         sv[k][rh][r] = y.x;
-                        mv[k][rh][r] = y.y;
+                        mv[k][rh][r] = fmaf(8.0f, y.x, y.y);  // (codes are taken from 8)
                         ri[k][rh][r] = rcp(y.x);
                     }
 #pragma unroll
@@ -634,10 +640,11 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                     for (int w = 0; w < 4; ++w) {  // dims 8 g + 2 w (rows g) and + 1 (rows g + 8)
                         const uint32_t x = __byte_perm(a0, a1, 0x0400 + 0x0101 * w);
                         const uint32_t y = __byte_perm(b0, b1, 0x0400 + 0x0101 * w);
+                        const uint32_t x0 = from_middle(x & 0x000f000fu, 0x00080008u), x1 = from_middle(x & 0x00f000f0u, 0x00800080u);
+                        const uint32_t y0 = from_middle(y & 0x000f000fu, 0x00080008u), y1 = from_middle(y & 0x00f000f0u, 0x00800080u);
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
-                            mma_f16(o[nb][h][w], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u,
-                                    pb[nb][h % GR][0], pb[nb][h % GR][1]);
+                            mma_f16(o[nb][h][w], x0, x1, y0, y1, pb[nb][h % GR][0], pb[nb][h % GR][1]);
                     }
                 }
             }

@@ -6,27 +6,32 @@
 //
 //   S = Q C_k^T         Q: rows scaled by powers of two into fp16, C_k: key codes
 //   z = f (S s_k + q' m_k)           f, q' = sum(q) per row, s_k, m_k per token
-//   w = fp16(2^(z - M + 7) mu)       value step s_v = mu 2^e, 1 <= mu < 2
-//   [O | L] += w [c_v 2^(e - e0) | 1/mu | m_v/mu 2^-e1]
+//   w = fp16(2^(z - M + 7) mu)       value step s_v = mu 2^e0 (see below)
+//   [O | L] += w [c_v - 8 | 1/mu | (m_v + 8 s_v)/mu 2^-e1]
 //
-// so that the output is (2^e0 O + 2^e1 L_m) / L_1: the divisor and the minima's
+// so that the output is (2^e0 O + 2^e1 L_m) / L_1: the divisor and the middles'
 // term are sums of the same rounded weights w as the codes' term, and the
 // rounding of a weight (2^-11 at most) changes how much a token counts, never
-// what it stands for.  1/mu and m_v/mu are pairs of fp16 (22 bits).  The
-// exponents e0, e1 follow the largest step and minimum so far (with room, so
-// that they hardly ever move; the sums are rescaled if they do).  A code of a
-// key is an fp16 subnormal masked out of its word (c 2^-24 or, the word's
-// upper half of a byte, 16 c 2^-24: Q takes the 16), of a value an fp16
-// 1024 + c brought to c 2^k by one fused multiply-add; both are exact.
+// what it stands for.  1/mu and the middles are pairs of fp16 (22 bits).  The
+// values' codes are taken from the middle because the tensor core's additions
+// round toward zero: sums of 0..15 drift with every step, and what is left of
+// them after the minima's term is small (0.0029 against 0.0017 relative error
+// over 9000 tokens, the latter being bf16's own; now 0.0017).
+// The exponents e0, e1 follow the largest step and middle so far, and the sums
+// are rescaled when they move; where steps differ by more than 2^9, part of a
+// step's exponent goes from the weight into the codes ((c_v - 8) 2^k).  A code
+// of a key is an fp16 subnormal masked out of its word (c 2^-24 or, the upper
+// half of a byte, 16 c 2^-24: Q takes the 16), of a value an fp16 1024 + c
+// brought to c - 8 by one fused multiply-add; both are exact.
 //
-// Roles of the 512 threads of a CTA (one per SM), which takes 256 columns
+// Roles of the 768 threads of a CTA (one per SM), which takes 256 columns
 // (pairs of query row and head of one key head) as two tiles of 128:
-//   warps 0-3, 4-7   softmax of a tile, a thread per row: S from TMEM, w back
-//                    to TMEM in the place of S, as the next product's A operand
-//   warps 8-10       values: one (token, group) per thread from 4 bits to fp16
-//   warps 11-13      the same for keys
-//   warp 14          issues the products (tcgen05.mma kind::f16)
-//   warp 15          copies pages (bulk copies of K and V codes and parameters)
+//   warps 0-7, 8-15  softmax of a tile of rows: S from TMEM as fragments of 16
+//                    rows, w back to TMEM in its place, as the next A operand
+//   warps 16-18      values: one (token, group) per thread from 4 bits to fp16
+//   warps 19-21      the same for keys
+//   warp 22          issues the products (tcgen05.mma kind::f16)
+//   warp 23          plans, and copies pages (bulk copies)
 // A tile of tokens is unpacked once for both tiles of rows, and the products
 // of one tile run while the other's softmax does.
 //
@@ -116,8 +121,7 @@ struct RowInfo {
 
 // What a tile of tokens tells the softmax beside its parameters.
 struct TileInfo {
-    int ue, uo;  // O holds the sums of even dims times 2^-ue, of odd dims times 2^-uo
-    int e1;      // and L the minima's times 2^-e1
+    int e0, e1;  // O holds sums times 2^-e0, L the middles' times 2^-e1
     int odd;     // holds values that are not finite
 };
 
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 m[i] = kNoMax;
                 sum[i] = 0.0f;
             }
-            int ue = 0, uo = 0, e1 = 0;
+            int e0 = 0, e1 = 0;
             for (int j = 0; j < g.tiles; ++j) {
                 const int tok0 = g.start + j * TOK;
                 const int buf = n & 1;
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                     if (!MODS) top[i] = fmaxf(top[i] * f[i], kNoMax);
                     rise |= top[i] > m[i] + kRise;
                 }
-                if (__any_sync(0xffffffffu, rise) || (j > 0 && (info.ue != ue || info.uo != uo || info.e1 != e1))) {
+                if (__any_sync(0xffffffffu, rise) || (j > 0 && (info.e0 != e0 || info.e1 != e1))) {
                     float keep[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -691,8 +695,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         sum[i] *= keep[i];
                     }
                     if (j > 0) {  // (the products up to here are complete: S came after them)
-                        // columns 2 t4, 2 t4 + 1 of 8: dims t4 and t4 + 4; of the sums: the divisor's, the minima's
-                        const float ko = t4 & 1 ? pow2i(uo - info.uo) : pow2i(ue - info.ue);
+                        // columns 2 t4, 2 t4 + 1 of 8; of the sums: the divisor's (t4 = 0), the middles'
+                        const float ko = pow2i(e0 - info.e0);
                         const float ks = t4 == 0 ? 1.0f : pow2i(e1 - info.e1);
 #pragma unroll 1
                         for (int c0 = 0; c0 < OC; c0 += 16) {
@@ -707,8 +711,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         }
                     }
                 }
-                ue = info.ue;
-                uo = info.uo;
+                e0 = info.e0;
                 e1 = info.e1;
 
 #pragma unroll
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 const RowInfo row = s_rows[c];
                 const bool spoilt = row.pos >= 0 && (!row.finite || row.pos >= g.cap);
                 if (row.pos >= g.cap) report(status, BQ_ERR_INVALID_ARG, SITE_KV4_ATTENTION);
-                const float we = pow2i(ue), wo = pow2i(uo), w1 = pow2i(e1);
+                const float w0 = pow2i(e0), w1 = pow2i(e1);
                 const int64_t row_out = (g.first + qrow) * a.q_heads + static_cast<int64_t>(g.head) * share + hh;
                 float *slot = ws.slots + (2 * cta + (g.begins ? 1 : 0)) * (static_cast<int64_t>(kCols) * (D + 4)) + c * (D + 4);
                 const uint32_t ot = tmem + C::T_O + tile * OC + (static_cast<uint32_t>(32 * wl) << 16);
@@ -819,7 +822,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {  // columns 0..7 of a block are dims 0 4 1 5 2 6 3 7
                         const int d = (i & 8) + ((i & 1) << 2) + ((i & 7) >> 1);
-                        v[d] = fmaf(__uint_as_float(o[i]), (i & 2) ? wo : we, lm) * inv;
+                        v[d] = fmaf(__uint_as_float(o[i]), w0, lm) * inv;
                     }
                     if (on && g.whole) {
                         uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row_out * D + d0 + h);
@@ -895,7 +898,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         codes(src, base + C::OFF_K + buf * C::KB + r * (G / 8) * (TOK * 16) + tok * 16);
                     } else {
                         // exponents of the tile (fp16's fields): each warp looks at all of its tokens
-                        uint32_t hi_s = 0, lo_s = 0x7c00u, hi_m = 0;
+                        uint32_t hi_s = 0, lo_s = 0x7c00u, hi_m = 0;  // (of s, s, m)
 #pragma unroll
                         for (int i = 0; i < TOK * GR / 32; ++i) {
                             const int k = i * 32 + lane, kt = k % TOK;
@@ -923,7 +926,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                             }
                             hi_s = __reduce_max_sync(0xffffffffu, hi_s);
                         }
-                        const int top0 = static_cast<int>(hi_s >> 10) - 15, top1 = static_cast<int>(hi_m >> 10) - 15;
+                        const int top0 = static_cast<int>(hi_s >> 10) - 15;
+                        const int top1 = max(static_cast<int>(hi_m >> 10) - 15, top0 + 3) + 1;  // of m + 8 s
                         if (j == 0) near = true;
                         if (j == 0 || top1 > e1 + 4) e1 = top1 - 2;
                         if (near) {
@@ -935,38 +939,49 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         const uint32_t vb = base + C::OFF_V + buf * C::VB + r * (G / 8 + 2) * (TOK * 16) + tok * 16;
                         const bool fit = held && !gone && fabsf(x.x) <= 65504.0f && fabsf(x.y) <= 65504.0f;
                         float mu = held && !gone && !fit ? __int_as_float(0x7fffffff) : 1.0f, inv = 0.0f, lm = 0.0f;
+                        auto scaled = [](uint32_t v, uint32_t by, uint32_t minus) {
+                            uint32_t d;
+                            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v | 0x64006400u), "r"(by), "r"(minus));
+                            return d;
+                        };
                         if (near) {
                             if (fit) {
                                 mu = x.x * pow2i(-e0);
                                 inv = rcp(mu);
-                                lm = x.y * pow2i(-e1) * inv;
+                                lm = fmaf(8.0f, x.x, x.y) * pow2i(-e1) * inv;
                             }
-                            codes(src, vb);
+#pragma unroll 1
+                            for (int i = 0; i < G / 32; ++i) {
+                                const int ch = (i + (tok >> (C::ROW == 64 ? 1 : 2))) & (G / 32 - 1);
+                                const uint4 v = lds128(src + ch * 16);
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int t = 0; t < 4; ++t)  // 1, -1032; 1 / 16, -72
+                                    sts128(vb + (ch * 4 + t) * (TOK * 16), scaled(w[t] & 0x000f000fu, 0x3c003c00u, 0xe408e408u),
+                                           scaled(w[t] & 0x00f000f0u, 0x2c002c00u, 0xd480d480u),
+                                           scaled((w[t] >> 8) & 0x000f000fu, 0x3c003c00u, 0xe408e408u),
+                                           scaled((w[t] >> 8) & 0x00f000f0u, 0x2c002c00u, 0xd480d480u));
+                            }
                         } else {
-                            uint32_t mult = 0, less = 0, mult16 = 0, less16 = 0;  // 2^k, -2^(k + 10), 2^(k - 4), -2^(k + 6)
+                            uint32_t mult = 0, less = 0, mult16 = 0, less16 = 0;  // 2^k, -1032 2^k, 2^(k - 4), -72 2^k
                             if (fit) {
                                 // a step far below e0's takes part of its exponent into the weight; what would
                                 // leave fp16 even so (below 2^-20 of the largest step) counts as 0
                                 const int k = max(exp_of(x.x) - e0, -20);
                                 mu = x.x * pow2i(-k - e0);
                                 inv = rcp(mu);
-                                lm = x.y * pow2i(-e1);
+                                lm = fmaf(8.0f, x.x, x.y) * pow2i(-e1);
                                 if (fabsf(inv) <= 32768.0f && fabsf(lm * inv) <= 32768.0f) {
                                     lm *= inv;
                                     const float b = pow2i(k);
                                     mult = pack_f16(b, b);
-                                    less = pack_f16(b * -1024.0f, b * -1024.0f);
+                                    less = pack_f16(b * -1032.0f, b * -1032.0f);
                                     mult16 = pack_f16(b * 0.0625f, b * 0.0625f);
-                                    less16 = pack_f16(b * -64.0f, b * -64.0f);
+                                    less16 = pack_f16(b * -72.0f, b * -72.0f);
                                 } else {
                                     mu = inv = 1.0f;
                                 }
                             }
-                            auto scaled = [](uint32_t v, uint32_t by, uint32_t minus) {
-                                uint32_t d;
-                                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v | 0x64006400u), "r"(by), "r"(minus));
-                                return d;
-                            };
 #pragma unroll 1
                             for (int i = 0; i < G / 8; ++i) {
                                 const uint32_t w = lds32(src + 4 * i);
@@ -980,7 +995,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         const float2 h = unpack_f16(hi);
                         const uint32_t lo = pack_f16(inv - h.x, lm - h.y);
                         sts128(vb + (G / 8) * (TOK * 16), __byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632), 0, 0);
-                        if (warp == 16 && lane == 0) s_info[buf] = {near ? e0 + 24 : e0, near ? e0 + 20 : e0, e1, odd ? 1 : 0};
+                        if (warp == 16 && lane == 0) s_info[buf] = {e0, e1, odd ? 1 : 0};
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
