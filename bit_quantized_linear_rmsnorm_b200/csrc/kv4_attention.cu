@@ -5,13 +5,18 @@
 // group of G elements of a token, so both leave the products:
 //
 //   q . K[t]   = sum_g s_k[t,g] (q_g . c[t,g]) + m_k[t,g] sum(q_g)
-//   sum p V[t] = sum_t (p_t s_v[t]) c[t] + sum_t p_t m_v[t]
+//   sum p V[t] = sum_t (p_t s_v[t]) (c[t] - 8) + sum_t p_t (m_v[t] + 8 s_v[t])
 //
 // and the matrix instructions (mma.sync m16n8k16, fp16 x fp16 -> fp32) see
 // the codes themselves.  A code masked in place out of its word, (w &
 // 0x000f000f) or (w & 0x00f000f0), is a pair of fp16 subnormals c * 2^-24 or
 // c * 2^-20, exact: two elements cost one AND and half a shift, and the powers
-// of two go into the query (odd codes' 2^4) and the final scale.  Keys are the A
+// of two go into the query (odd codes' 2^4) and the final scale.  Values' codes
+// are taken from the middle (one subtraction for two, exact): the instruction's
+// additions round toward zero, and sums of 0..15 drift with every step while the
+// result is what the minima's term leaves of them (one row over 131072 tokens:
+// relative error 0.0018 against 0.0016 of a 32-bit computation rounded to bf16;
+// now the same).  Keys are the A
 // operand of K q^T (rows: 16 tokens), values that of V^T p (rows: 16 dims),
 // so 8 columns carry the query rows and heads that share a key head, and p
 // moves from one product to the next by two 8 x 8 register transposes.
@@ -21,19 +26,29 @@
 // the type of the instruction; the sums that go with it (the divisor, and
 // the minima's term) are taken of the same rounded weights, so the rounding
 // acts as a relative error of a weight, 2^-11 at most, and cancels for a
-// single token.  Running maximum, sums and products are fp32.  The maximum is
+// single token.  (A step far below the others' would leave fp16's range with
+// its weight: such a token counts in the sums with its weight as it is.)
+// Running maximum, sums and products are fp32.  The maximum is
 // that of z + log2 s_v, which keeps p * s_v within fp16 whatever the steps
 // are; it is raised only when a score passes it by 2^8 (the weights then stay
 // below 2^15), so most tiles need no shuffles and no rescaling.
 //
 // Work.  The tiles (32 tokens of one key head and column block) of the whole
-// batch are one list, cut into equal shares for the CTAs, whatever the
-// lengths are: two CTAs per SM (one where more columns take the registers),
-// 8 warps each, every warp with a ring of tiles of its own that bulk copies
-// fill.  The warps of a share meet in shared memory; a (sequence, head,
-// columns) item that spans several CTAs leaves partial results in the
-// workspace, and a second kernel, launched as a programmatic dependent, joins
-// them.
+// batch, and kStart tiles' worth for beginning an item, are one list, cut into
+// equal shares for the CTAs, whatever the lengths are: three CTAs per SM (two
+// where more columns take the registers), 4 warps each, every warp with a ring
+// of tiles of its own that bulk copies fill.  The warps of a share meet in
+// shared memory; a (sequence, head, columns) item that spans several CTAs
+// leaves partial results in the workspace, and a second kernel, launched as a
+// programmatic dependent, joins them.
+//
+// What bounds it: DRAM traffic is the cache read once (321 MB for 64 ragged
+// sequences of up to 8192 tokens, 8 heads of 128), but at 102 us (48% of the
+// measured copy bandwidth) it is the issue of instructions: about 720 for a
+// tile, of which 192 bring codes into registers, at 57% of the issue slots,
+// the rest being fixed latencies of 12 warps.  Measured against this split:
+// two CTAs of 8 warps (128 registers, addresses worked out again for each
+// tile) 119 us; copies by cp.async of all lanes 122 us; without kStart 129 us.
 //
 // Every wait on a copy is bounded; if one runs out, the kernel records
 // BQ_ERR_TIMEOUT, lets its copies land (bounded again) and finishes.
@@ -48,7 +63,7 @@ constexpr int kTile = 32;
 constexpr int kW = 4;  // warps
 constexpr int kThreads = kW * 32;
 constexpr int kStart = 6;  // cost of starting an item, in tiles
-constexpr float kSlack = 8.0f;      // a maximum is raised when passed by more
+constexpr float kSlack = 8.0f;  // a maximum is raised when passed by more
 constexpr float kFarStep = 0.001953125f;  // a step below 2^-9 of the largest is far from it
 
 // (D, G) shape of the cache and the geometry that follows from it.
