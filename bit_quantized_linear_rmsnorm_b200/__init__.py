@@ -10,6 +10,7 @@ the library is missing or the device is not sm_100, calls fail loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -556,6 +557,7 @@ def bq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Te
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def bq_kv4_attention_workspace_bytes(total: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().bq_kv4_attention_workspace_bytes(total, q_heads, kv_heads, head_dim))
 

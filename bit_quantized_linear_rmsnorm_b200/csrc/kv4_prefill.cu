@@ -648,18 +648,21 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                     const float cap2 = a.softcap * 1.4426950408889634f;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint64_t f2 = pack64(f[i], f[i]);
+                        const uint64_t f2 = pack64(f[i], f[i]), slopes = pack64(slope2[i], slope2[i]);
                         const float away = static_cast<float>(tok0 + 2 * t4 - pos[i]);
+                        const uint64_t bias = pack64(slope2[i] * away, slope2[i] * (away + 1.0f));
+                        if (a.softcap > 0.0f) {  // cap tanh(x) = cap (1 - 2 / (exp(2 x) + 1))
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            float2 z = unpack64(mul2(y[b][i], f2));
-                            if (a.softcap > 0.0f) {  // cap tanh(x) = cap (1 - 2 / (exp(2 x) + 1))
-                                z.x = fmaf(-2.0f * cap2, rcp(ex2(z.x) + 1.0f), cap2);
-                                z.y = fmaf(-2.0f * cap2, rcp(ex2(z.y) + 1.0f), cap2);
+                            for (int b = 0; b < NB; ++b) {
+                                const float2 z = unpack64(mul2(y[b][i], f2));
+                                const float2 d = unpack64(fma2(slopes, pack64(8.0f * b, 8.0f * b), bias));
+                                y[b][i] = pack64(fmaf(-2.0f * cap2, rcp(ex2(z.x) + 1.0f), cap2) + d.x,
+                                                 fmaf(-2.0f * cap2, rcp(ex2(z.y) + 1.0f), cap2) + d.y);
                             }
-                            z.x = fmaf(slope2[i], away + static_cast<float>(8 * b), z.x);
-                            z.y = fmaf(slope2[i], away + static_cast<float>(8 * b + 1), z.y);
-                            y[b][i] = pack64(z.x, z.y);
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+                                y[b][i] = fma2(y[b][i], f2, fma2(slopes, pack64(8.0f * b, 8.0f * b), bias));
                         }
                     }
                 }
