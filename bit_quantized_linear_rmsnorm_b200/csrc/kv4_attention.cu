@@ -43,7 +43,7 @@
 // programmatic dependent, joins them.
 //
 // What bounds it: DRAM traffic is the cache read once (321 MB for 64 ragged
-// sequences of up to 8192 tokens, 8 heads of 128), but at 102 us (48% of the
+// sequences of up to 8192 tokens, 8 heads of 128), but at 98 us (50% of the
 // measured copy bandwidth) it is the issue of instructions: about 720 for a
 // tile, of which 192 bring codes into registers, at 57% of the issue slots,
 // the rest being fixed latencies of 12 warps.  Measured against this split:
@@ -62,7 +62,7 @@ namespace {
 constexpr int kTile = 32;
 constexpr int kW = 4;  // warps
 constexpr int kThreads = kW * 32;
-constexpr int kStart = 6;  // cost of starting an item, in tiles
+constexpr int kStart = 12;  // cost of starting an item, in tiles (64 ragged sequences: 115, 109, 105, 102 us at 3, 6, 10, 14)
 constexpr float kSlack = 8.0f;  // a maximum is raised when passed by more
 constexpr float kFarStep = 0.001953125f;  // a step below 2^-9 of the largest is far from it
 
@@ -77,7 +77,7 @@ struct Shape {
     static constexpr int CODES = kTile * ROW, PARS = kTile * PAR;
     static constexpr int STAGE = 2 * (CODES + PARS);
     static constexpr int CTAS = NB == 1 ? 3 : 2;  // per SM
-    static constexpr int S = NB == 1 ? 4 : 5;  // stages of a warp
+    static constexpr int S = NB == 1 ? 3 : 5;  // stages of a warp (a fourth gains nothing)
     static constexpr int COLS = 8 * NB;
     static constexpr int CSTR = D + 8;  // floats between columns of a warp's results
     static constexpr int RES = (COLS * CSTR + COLS * (2 + GR)) * 4;  // bytes of a warp's results

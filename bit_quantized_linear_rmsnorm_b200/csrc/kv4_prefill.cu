@@ -204,14 +204,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {  // M
     return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(kRows >> 4) << 24);
 }
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t *r) {
-    static_assert(N == 32 || N == 16, "");
-    if constexpr (N == 32)
-        tmem_ld_32x32b_x32(a, *reinterpret_cast<uint32_t(*)[32]>(r));
-    else
-        tmem_ld_32x32b_x16(a, *reinterpret_cast<uint32_t(*)[16]>(r));
-}
 // 16 lanes x 8 N columns as the fragments of a matrix product: of each 8
 // columns, lane 4 g + t holds columns 2 t, 2 t + 1 of rows g and g + 8.
 template <int N>
@@ -819,7 +811,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 const uint32_t ot = tmem + C::T_O + tile * OC + (static_cast<uint32_t>(32 * wl) << 16);
                 const int grp = GR == 1 ? 0 : hw;
                 uint32_t l[16];
-                tmem_ld<16>(ot + grp * (G + 16) + G, l);
+                tmem_ld_32x32b_x16(ot + grp * (G + 16) + G, l);
                 tmem_wait_ld();
                 float den = __uint_as_float(l[0]) + __uint_as_float(l[1]), row_sum = row.sum;
                 const float lm = (__uint_as_float(l[2]) + __uint_as_float(l[3])) * w1;
@@ -830,7 +822,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
 #pragma unroll
                 for (int h = 0; h < D / 2; h += 16) {
                     uint32_t o[16];
-                    tmem_ld<16>(ot + (GR == 1 ? d0 : grp * (G + 16)) + h, o);
+                    tmem_ld_32x32b_x16(ot + (GR == 1 ? d0 : grp * (G + 16)) + h, o);
                     tmem_wait_ld();
                     float v[16];
 #pragma unroll
