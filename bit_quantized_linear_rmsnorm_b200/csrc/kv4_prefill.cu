@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 k = min(k, 120);
                 const float up = !finite ? 0.0f : copysignf(__uint_as_float(static_cast<uint32_t>(127 + k) << 23), a.scale);
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                // codes are c 2^-24; (not 0, so that what is hidden ends up far below what is seen)
+                // codes are c 2^-24; (not 0: a hidden score is -inf before it meets this factor, and stays that)
                 float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * down * 16777216.0f, 7.8886090522101181e-31f);
                 if (MODS && a.softcap > 0.0f) f *= 2.0f / a.softcap;  // the argument of tanh, times 2 log2(e)
                 const uint32_t dst = base + C::OFF_Q + tile * C::QB + part * (D / 16) * (kRows * 16) + row * 16;
@@ -670,23 +670,24 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
                             float2 z = unpack64(y[b][i]);
-                            if (8 * b > see_hi[i] || 8 * b < see_lo[i]) z.x = kNoMax;
-                            if (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i]) z.y = kNoMax;
+                            if (8 * b > see_hi[i] || 8 * b < see_lo[i]) z.x = -INFINITY;
+                            if (8 * b + 1 > see_hi[i] || 8 * b + 1 < see_lo[i]) z.y = -INFINITY;
                             y[b][i] = pack64(z.x, z.y);
                         }
                     }
                 }
+                // (a row that has seen nothing keeps m = kNoMax, which is finite: its weights are 2^-inf = 0, whatever f is)
                 float top[2];
                 bool rise = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    top[i] = kNoMax;
+                    top[i] = -INFINITY;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         const float2 z = unpack64(y[b][i]);
                         top[i] = fmaxf(top[i], fmaxf(z.x, z.y));
                     }
-                    if (!MODS) top[i] = fmaxf(top[i] * f[i], kNoMax);
+                    if (!MODS) top[i] *= f[i];
                     rise |= top[i] > m[i] + kRise;
                 }
                 if (__any_sync(0xffffffffu, rise) || (j > 0 && (info.e0 != e0 || info.e1 != e1))) {

@@ -1,0 +1,96 @@
+"""The 4-bit cache's attention where its arithmetic and its bookkeeping have borders: rows that see nothing, in a tile or at
+all, queries and values far from one, places behind a window, positions at the ends of their range, other streams.
+
+Yardstick and bounds are those of test_gpu_kv4.py (kv4_reference.py) unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_linear_rmsnorm_b200 as bq
+import kv4_reference as ref
+from test_gpu_kv4 import DT, SHAPES, Setup, check_attention, dev, offsets, query, run_attention, status_ok
+
+pytestmark = pytest.mark.gpu
+
+EXTRAS = [dict(), dict(softcap=5.0), dict(slopes=1), dict(window=7), dict(window=33, softcap=20.0, slopes=1)]
+
+
+def extras(kw, heads):
+    return dict(kw, slopes=2.0 ** -np.linspace(1.0, 8.0, heads)) if "slopes" in kw else kw
+
+
+def check_lse(s, lse, q, cu, scale, **kw):
+    """lse against the yardstick, for scores of any size.
+
+    d lse = sum p dz, so |error of lse| <= max |error of z| + that of the weights (2^-11 each, at most, on the sum that the
+    logarithm is taken of) and of the logarithm itself: 2^-10 + 2^-20 |lse| for these two, as in check_attention.  A
+    score's error is kv4_reference's: a dot product of D terms and the minimum's term in fp32, one step u = 2^-23 each,
+    (D + 16) u |scale| sum|q| (15 s + |m|), and 4 u |z|, where |z| <= |scale| sum|q| (15 s + |m|) too."""
+    _, want, _ = ref.attention(q.double().cpu().numpy(), s.host, s.table, s.lens, cu, scale, **kw)
+    got = lse.double().cpu().numpy()[: int(cu[-1])]
+    want = want[: len(got)]
+    assert np.array_equal(np.isneginf(got), np.isneginf(want)) and np.array_equal(np.isnan(got), np.isnan(want))
+    most = 0.0
+    for b, n in enumerate(s.lens):
+        par = s.host._part(0)[1][s.table[b, : -(-n // s.page)].astype(np.int64)].astype(np.float64)
+        par = (15 * par[..., 0] + np.abs(par[..., 1])).transpose(0, 2, 1, 3).reshape(-1, s.H, par.shape[-2])[:n]
+        most = max(most, par.max(initial=0.0))
+    dz = (s.D + 16 + 4) * 2.0 ** -23 * abs(scale) * q.double().abs().sum(-1).cpu().numpy()[: len(got)] * most
+    fin = np.isfinite(want)
+    bad = np.abs(got[fin] - want[fin]) > (2.0 ** -10 + 2.0 ** -20 * np.abs(want) + dz)[fin]
+    assert not bad.any()
+
+
+# ------------------------------------------------------------------ rows that see nothing of a tile, or nothing at all
+@pytest.mark.parametrize("size", [1e-30, 1e-3, 0.006, 300.0])
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_many_rows_with_queries_of_every_size(D, G, size):
+    """The first tiles of an item hold nothing for its last rows (a window, one head to a key head), whatever the factor
+    between a product and its score is."""
+    s = Setup([200], 1, D, G, 32, seed=20).fill()
+    pool, table, lens = s.cuda(), dev(s.table), dev(s.lens)
+
+    def check(q, scale=D ** -0.5, **kw):
+        lse = torch.full((200, 1), 3.0, device="cuda")
+        out = bq.bq_kv4_attention(q, pool, table, lens, G, scale=scale, lse=lse, **kw)
+        check_attention(s, out, None, q, [0, 200], scale, **kw)
+        check_lse(s, lse, q, [0, 200], scale, **kw)
+        assert torch.equal(bq.bq_kv4_attention(q, pool, table, lens, G, scale=scale, **kw), out)  # without lse
+
+    q = query(s, 200, 1, "bf16", scale=size)
+    for window in (16, 70, 0):
+        check(q, window=window)
+    q[::3] *= 2.0 ** -12  # rows of different sizes in one tile
+    check(q, window=70)
+    for scale in (0.01, -0.001):
+        check(q, scale, window=16)
+    status_ok()
+
+
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_items_cut_between_ctas_with_small_queries(D, G):
+    """The last part of a cut item holds nothing for its first rows."""
+    s = Setup([2500, 130], 1, D, G, 64, seed=21).fill()
+    for counts, heads in (([200, 5], 1), ([30, 100], 4)):
+        q = query(s, sum(counts), heads, "bf16", scale=1e-3)
+        run_attention(s, q, counts)
+        run_attention(s, q, counts, window=900)
+
+
+@pytest.mark.parametrize("kw", EXTRAS)
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_many_rows_without_a_place_and_empty_slots(D, G, kw):
+    """Rows before position 0 in an item whose other rows see tokens, a sequence of length 0, a padded slot: 0 and -inf."""
+    kw = extras(kw, 4)
+    s = Setup([35, 0, 0, 50], 1, D, G, 16, seed=22).fill()
+    counts = [40, 30, 0, 12]
+    for dtype, size in (("f16", 1.0), ("bf16", 1e-3)):
+        out = run_attention(s, query(s, sum(counts) + 3, 4, dtype, scale=size), counts, rows_behind=3, **kw)
+        assert (out[:5] == 0).all() and (out[40:70] == 0).all() and (out[5:40] != 0).any()
+    # at once too small for its rows and alone in its call
+    s = Setup([3], 1, D, G, 16, seed=23).fill()
+    out = run_attention(s, query(s, 300, 4, "bf16"), [300], **kw)
+    assert (out[:297] == 0).all()
+    # the few-row kernel gives the same
+    s = Setup([2, 0], 1, D, G, 16, seed=24).fill()
+    run_attention(s, query(s, 8, 4, "bf16"), [4, 4], **kw)
