@@ -126,8 +126,8 @@ __device__ __forceinline__ SeqPlan plan_seq(const Kv4AttnArgs &a, int b, int sha
     p.rows = static_cast<int>(min(static_cast<int64_t>(min(n, a.max_q)), a.total - p.first));
     if (n <= 0 || p.rows < 0 || p.first < 0) p.rows = 0;
     p.pos0 = static_cast<int>(max(static_cast<int64_t>(len) - n, static_cast<int64_t>(-0x7fffffff)));
-    const int64_t cap = min(static_cast<int64_t>(a.pool.table_width) << a.pool.page_log2, int64_t(0x7fffffff));
-    p.hi = static_cast<int>(min(static_cast<int64_t>(p.pos0) + p.rows, cap)) - 1;
+    const int cap = kv4_capacity(a.pool);
+    p.hi = static_cast<int>(min(static_cast<int64_t>(p.pos0) + p.rows, static_cast<int64_t>(cap))) - 1;
     const int lo = a.window > 0 ? static_cast<int>(max(static_cast<int64_t>(p.pos0) - a.window + 1, int64_t(0))) : 0;
     if (p.hi < lo) p.hi = -1;
     p.t0 = lo / kTile;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
         const int ntiles = static_cast<int>((seg_end - item_begin) * p.tiles / item_cost - first_tile);
         const int col0 = cb * C::COLS;  // columns: row of the sequence * share + head of the group
         const int ncols = min(C::COLS, p.rows * share - col0);
-        const int64_t cap = min(static_cast<int64_t>(a.pool.table_width) << page_log2, int64_t(0x7fffffff));
+        const int cap = kv4_capacity(a.pool);
 
         // ---- the warp's own tiles: tile0 + warp, + kW, ...; their pages are
         // looked up 32 tiles ahead, a lane each

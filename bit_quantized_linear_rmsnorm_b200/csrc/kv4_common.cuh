@@ -42,6 +42,14 @@ __device__ __forceinline__ void kv4_rows(const Kv4Seqs &s, int b, int64_t &first
     }
 }
 
+// Positions that attention reaches: those of the table, and no more than leave
+// room above them, so that the first token of a tile, of a copy, or of a page
+// looked up ahead is a 32-bit number for every tile that begins below.
+constexpr int kKv4MaxTokens = 0x7fff0000;
+__device__ __forceinline__ int kv4_capacity(const Kv4Pool &p) {
+    return static_cast<int>(min(static_cast<int64_t>(p.table_width) << p.page_log2, static_cast<int64_t>(kKv4MaxTokens)));
+}
+
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));

@@ -492,6 +492,7 @@ bq_status bq_bitlinear_w2a8_noalloc(const void *x, bq_dtype x_dtype, int64_t M, 
  *     position behind the table, records BQ_ERR_INVALID_ARG in the device
  *     status word; the call then skips (write) or gives NaN for (read,
  *     attention) what it would have held, and touches no other memory.
+ *     (Attention counts positions from 2^31 - 65536 on as behind the table.)
  *   cu_q: int32 [batch + 1], the rows of sequence b being cu_q[b] up to
  *     cu_q[b+1] (cu_q[0] = 0, not decreasing, cu_q[batch] <= total); or NULL:
  *     total / batch rows each (total must be a multiple of batch).  Rows

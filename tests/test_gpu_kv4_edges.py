@@ -94,3 +94,28 @@ def test_many_rows_without_a_place_and_empty_slots(D, G, kw):
     # the few-row kernel gives the same
     s = Setup([2, 0], 1, D, G, 16, seed=24).fill()
     run_attention(s, query(s, 8, 4, "bf16"), [4, 4], **kw)
+
+
+# ------------------------------------------------------------------ positions at the ends of their range
+def test_positions_near_the_end_of_32_bits():
+    """A table as wide as positions go (2^24 pages of 128).  Up to 2^31 - 65537 a row is attended to as anywhere else;
+    from there on it stands behind the table: NaN, reported, and no page is looked up outside the table."""
+    page, G = 128, 64
+    s = Setup([1024], 1, 64, G, page, seed=25).fill()
+    pool = s.cuda()
+    wide = dev(s.table[0, :8]).repeat(1 << 21)[None].contiguous()  # the small sequence's 8 pages over and over
+    most = (1 << 31) - 65536
+    for n, heads in ((1, 2), (200, 2)):
+        q = query(s, n, heads, "bf16")
+        out = bq.bq_kv4_attention(q, pool, wide, dev([most]), G, window=64)  # (most is a multiple of 1024)
+        check_attention(s, out, None, q, [0, n], 64 ** -0.5, window=64)
+        status_ok()
+        # the last rows of 31 bits; with n = 200 some begin in a tile that would end behind them
+        out = bq.bq_kv4_attention(q, pool, wide, dev([(1 << 31) - 1]), G, window=1)
+        assert bq.bq_device_status()[0] == bq.BQ_ERR_INVALID_ARG and out.isnan().all()
+        out = bq.bq_kv4_attention(q, pool, wide, dev([most + n // 2]), G, window=64)
+        assert bq.bq_device_status()[0] == (bq.BQ_ERR_INVALID_ARG if n > 1 else bq.BQ_OK)
+        if n > 1:
+            assert out[n - n // 2:].isnan().all()
+            keep = q[: n - n // 2]
+            check_attention(s, out[: n - n // 2].contiguous(), None, keep, [0, len(keep)], 64 ** -0.5, window=64)
