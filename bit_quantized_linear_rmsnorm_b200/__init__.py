@@ -505,6 +505,15 @@ def _kv4_strides(t: torch.Tensor):
     return (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
+def _kv4_empty(shape, dtype, device, stream):
+    """torch.empty for a call that launches on `stream`: allocated on that stream, so that the caching allocator hands
+    the bytes out again only behind the call's kernels (and takes none that another stream still uses)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _kv4_call(dev: int, fn, stream, *args):
     """fn(*args, stream handle) with device `dev` current (the library launches on the current device)."""
     if dev == torch.cuda.current_device():
@@ -539,14 +548,14 @@ def bq_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_ta
 def bq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Tensor, total: int, head_dim: int,
                 group_size: int, starts=None, out_dtype=torch.bfloat16, k=None, v=None, stream=None):
     """(k, v) [total, kv_heads, D]: positions starts[b] + j (starts None: 0) of each sequence, its rows cu_len[b] up
-    to cu_len[b + 1]."""
+    to cu_len[b + 1].  Outputs that are not given are allocated on `stream`."""
     pages, pstride, page, H = _kv4_cache(cache, head_dim, group_size, block_table, cu_len, starts)
     B, ld, width = _kv4_batch(block_table, None, cu_len, starts)
     shape, dev = (total, H, head_dim), cache.get_device()
     if k is None:
-        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
+        k = _kv4_empty(shape, out_dtype, cache.device, stream)
     if v is None:
-        v = torch.empty_like(k)
+        v = _kv4_empty(shape, k.dtype, cache.device, stream)
     if k.shape != shape or v.shape != shape or k.dtype is not v.dtype or k.dtype not in _DTYPE or \
             not (k.is_contiguous() and v.is_contiguous()) or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("k and v must be dense [total, kv_heads, head_dim] of one type on the cache's device")
@@ -567,7 +576,8 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
                      slopes=None, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of q [T, q_heads, D] over a 4-bit cache: each sequence's rows stand at the end of its
     seq_lens tokens.  cu_q [batch + 1] gives the rows of each sequence (None: T / batch each), max_q the most rows of
-    one (None: T).  Returns out [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given."""
+    one (None: T).  Returns out [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given.  What is not given
+    (out, the workspace) is allocated on `stream`; calls that run at the same time need a workspace each."""
     dev = cache.get_device()
     if q.dim() != 3 or q.get_device() != dev or q.dtype not in _DTYPE or (q.numel() and q.stride(2) != 1):
         raise ValueError("expected q [T, q_heads, D], dense along D, on the cache's device")
@@ -575,7 +585,7 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
     pages, pstride, page, H = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
     B, ld, width = _kv4_batch(block_table, seq_lens, cu_q)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        out = _kv4_empty((T, Hq, D), q.dtype, q.device, stream)
     elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be dense, of q's shape, type and device")
     if slopes is not None and (slopes.dtype is not torch.float32 or slopes.shape != (Hq,) or
@@ -585,7 +595,7 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
                             not lse.is_contiguous()):
         raise ValueError("lse must be dense fp32 [T, q_heads] on q's device")
     if workspace is None:
-        workspace = torch.empty(bq_kv4_attention_workspace_bytes(T, Hq, H, D), dtype=torch.uint8, device=q.device)
+        workspace = _kv4_empty(bq_kv4_attention_workspace_bytes(T, Hq, H, D), torch.uint8, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be dense and on q's device")
     qt, qh = _kv4_strides(q)

@@ -119,3 +119,30 @@ def test_positions_near_the_end_of_32_bits():
             assert out[n - n // 2:].isnan().all()
             keep = q[: n - n // 2]
             check_attention(s, out[: n - n // 2].contiguous(), None, keep, [0, len(keep)], 64 ** -0.5, window=64)
+
+
+# ------------------------------------------------------------------ other streams than the current one
+@pytest.mark.parametrize("n", [1, 50])
+def test_calls_that_overlap_on_streams_given_to_them(n):
+    """No workspace or output given, nothing waited for between the calls: each has its own, and what the current stream
+    allocates meanwhile is not written to."""
+    s = Setup([5000, 300, 4000], 2, 128, 64, 64, seed=26).fill()
+    pool, table, lens = s.cuda(), dev(s.table), dev(s.lens)
+    qs = [query(s, 3 * n, 8, "bf16") for _ in range(2)]
+    want = [bq.bq_kv4_attention(q, pool, table, lens, s.G) for q in qs]
+    cu = dev(offsets(s.lens))
+    kv = bq.bq_kv4_read(pool, table, cu, 9300, 128, 64)
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    size = bq.bq_kv4_attention_workspace_bytes(3 * n, 8, 2, 128)
+    for _ in range(5):
+        got, other, reads = [], [], []
+        for q, st in zip(qs, side):
+            got.append(bq.bq_kv4_attention(q, pool, table, lens, s.G, stream=st))
+            other.append(torch.full((size,), 7, dtype=torch.uint8, device="cuda"))  # (on the current stream)
+            reads.append(bq.bq_kv4_read(pool, table, cu, 9300, 128, 64, stream=st))
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(got[i], want[i]) and (other[i] == 7).all()
+            assert torch.equal(reads[i][0], kv[0]) and torch.equal(reads[i][1], kv[1])
+    status_ok()

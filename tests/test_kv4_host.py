@@ -133,6 +133,62 @@ def test_binding_refuses_what_does_not_fit():
             f()
 
 
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is on GPU 0, for what the binding does before the library's call."""
+
+    def get_device(self):
+        return 0
+
+
+def on_device(t):
+    return t.as_subclass(OnDevice)
+
+
+def test_allocations_follow_the_stream(monkeypatch):
+    """Outputs and workspace that a call allocates belong to the stream that it launches on: two calls on two streams
+    never share one, and none is handed out again before the call's kernels have run."""
+    import contextlib
+
+    class Stream:
+        cuda_stream = 0
+
+        def __init__(self, name):
+            self.name = name
+
+    now, made, given = ["current"], [], []
+    empty = torch.empty
+
+    @contextlib.contextmanager
+    def enter(stream):
+        now.append(stream.name)
+        yield
+        now.pop()
+
+    def watched(*args, **kw):
+        t = empty(*args, **kw)
+        made.append((now[-1], t))
+        return on_device(t)
+
+    def call(dev, fn, stream, *args):
+        given.append(None if stream is None else stream.name)
+        return bq.BQ_OK
+
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch, "empty", watched)
+    monkeypatch.setattr(torch, "empty_like", lambda t, **kw: watched(t.shape, dtype=t.dtype, device=t.device))
+    monkeypatch.setattr(bq, "_kv4_call", call)
+    cache = on_device(torch.zeros(3, 2, ref.page_bytes(16, 64, 64), dtype=torch.uint8))
+    table, lens = (on_device(torch.ones(s, dtype=torch.int32)) for s in ((2, 1), (2,)))
+    cu = on_device(torch.tensor([0, 1, 2], dtype=torch.int32))
+    q = on_device(torch.zeros(2, 4, 64).bfloat16())
+    for stream, name in ((None, "current"), (Stream("a"), "a"), (Stream("b"), "b")):
+        for fn, count in ((lambda: bq.bq_kv4_attention(q, cache, table, lens, 64, stream=stream), 2),
+                          (lambda: bq.bq_kv4_read(cache, table, cu, 2, 64, 64, stream=stream), 2)):
+            del made[:], given[:]
+            fn()
+            assert [m[0] for m in made] == [name] * count and given == [stream and name]
+
+
 # ------------------------------------------------------------------ pins of the yardstick
 def test_quantize_by_hand():
     # minimum 0, maximum 15: step 1, so a value is its own code and k + 1/2 goes to the even neighbour
