@@ -154,11 +154,20 @@ def bq_device_status(stream=None):
     return st, detail.value
 
 
-def _workspace(nbytes: int, device, workspace=None):
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call that launches on `stream`: allocated on that stream, so that the caching allocator hands
+    the bytes out again only behind the call's kernels (and takes none that another stream still uses)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(nbytes: int, device, workspace, stream):
     if workspace is not None:
         return workspace
     # 256-byte aligned (the caching allocator returns >= 512-byte aligned blocks)
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return _empty(max(nbytes, 1), torch.uint8, device, stream)
 
 
 def bq_act_quant_int8(x: torch.Tensor, eps: float = 1e-5, xq=None, act_scale=None, rowsum=None,
@@ -167,11 +176,11 @@ def bq_act_quant_int8(x: torch.Tensor, eps: float = 1e-5, xq=None, act_scale=Non
     M, K = x.shape
     if xq is None:
         ldq = (K + 15) // 16 * 16
-        xq = torch.empty((M, ldq), dtype=torch.int8, device=x.device)[:, :K]
+        xq = _empty((M, ldq), torch.int8, x.device, stream)[:, :K]
     if act_scale is None:
-        act_scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        act_scale = _empty(M, torch.float32, x.device, stream)
     if rowsum is None and want_rowsum:
-        rowsum = torch.empty(M, dtype=torch.int32, device=x.device)
+        rowsum = _empty(M, torch.int32, x.device, stream)
     st = lib().bq_act_quant_int8(_ptr(x), _DTYPE[x.dtype], M, K, _ld(x), float(eps), _ptr(xq), _ld(xq),
                                  _ptr(act_scale), _ptr(rowsum), _stream(stream))
     _check(st, "bq_act_quant_int8")
@@ -185,11 +194,11 @@ def bq_act_quant_int8_layernorm(x: torch.Tensor, eps: float = 1e-5, ln_weight=No
     M, K = x.shape
     if xq is None:
         ldq = (K + 15) // 16 * 16
-        xq = torch.empty((M, ldq), dtype=torch.int8, device=x.device)[:, :K]
+        xq = _empty((M, ldq), torch.int8, x.device, stream)[:, :K]
     if act_scale is None:
-        act_scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        act_scale = _empty(M, torch.float32, x.device, stream)
     if rowsum is None and want_rowsum:
-        rowsum = torch.empty(M, dtype=torch.int32, device=x.device)
+        rowsum = _empty(M, torch.int32, x.device, stream)
     st = lib().bq_act_quant_int8_layernorm(_ptr(x), _DTYPE[x.dtype], M, K, _ld(x), _ptr(ln_weight), _ptr(ln_bias),
                                            float(eps), _ptr(xq), _ld(xq), _ptr(act_scale), _ptr(rowsum),
                                            _stream(stream))
@@ -203,9 +212,9 @@ def bq_bitlinear_w2a8_layernorm(x: torch.Tensor, wpacked: torch.Tensor, w_scale:
     """BitLinear forward with the LayerNorm normaliser."""
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = _empty((M, N), out_dtype, x.device, stream)
     nbytes = bq_workspace_bytes(BQ_OP_BITLINEAR_W2A8, M, N, K)
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     st = lib().bq_bitlinear_w2a8_layernorm(_ptr(x), _DTYPE[x.dtype], M, K, _ptr(ln_weight), _ptr(ln_bias),
                                            _ptr(wpacked), _ptr(w_scale), N, _ptr(bias), float(eps), _DTYPE[out.dtype],
                                            _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -217,11 +226,11 @@ def bq_weight_quant_ternary_pack(w: torch.Tensor, wpacked=None, w_scale=None, wo
     """(wpacked uint32-as-int32 [N,K/16], w_scale fp32 [1])."""
     N, K = w.shape
     if wpacked is None:
-        wpacked = torch.empty((N, K // 16), dtype=torch.int32, device=w.device)
+        wpacked = _empty((N, K // 16), torch.int32, w.device, stream)
     if w_scale is None:
-        w_scale = torch.empty(1, dtype=torch.float32, device=w.device)
+        w_scale = _empty(1, torch.float32, w.device, stream)
     nbytes = bq_workspace_bytes(BQ_OP_WEIGHT_QUANT_TERNARY_PACK, 0, N, K)
-    ws = _workspace(nbytes, w.device, workspace)
+    ws = _workspace(nbytes, w.device, workspace, stream)
     st = lib().bq_weight_quant_ternary_pack(_ptr(w), _DTYPE[w.dtype], N, K, _ptr(wpacked), _ptr(w_scale),
                                             _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "bq_weight_quant_ternary_pack")
@@ -234,9 +243,9 @@ def bq_weight_pack_int4_grouped(q: torch.Tensor, zeros: torch.Tensor, group_size
     N, K = q.shape
     G = K // group_size
     if qweight is None:
-        qweight = torch.empty((N, K // 8), dtype=torch.int32, device=q.device)
+        qweight = _empty((N, K // 8), torch.int32, q.device, stream)
     if qzeros is None:
-        qzeros = torch.empty((N, (G + 7) // 8), dtype=torch.int32, device=q.device)
+        qzeros = _empty((N, (G + 7) // 8), torch.int32, q.device, stream)
     st = lib().bq_weight_pack_int4_grouped(_ptr(q), _ptr(zeros), N, K, group_size, _ptr(qweight), _ptr(qzeros),
                                            _stream(stream))
     _check(st, "bq_weight_pack_int4_grouped")
@@ -252,7 +261,7 @@ def bq_gemm_i8_pertoken(x: torch.Tensor, w: torch.Tensor, deq_scale: torch.Tenso
         esz = torch.tensor([], dtype=out_dtype).element_size()
         pad = 16 // esz
         ldo = (N + pad - 1) // pad * pad
-        out = torch.empty((M, ldo), dtype=out_dtype, device=x.device)[:, :N]
+        out = _empty((M, ldo), out_dtype, x.device, stream)[:, :N]
     st = lib().bq_gemm_i8_pertoken(_ptr(x), _ld(x), _ptr(w), w_layout, _ld(w), _ptr(deq_scale),
                                    _ptr(per_token_scale), _ptr(bias), M, N, K, _DTYPE[out.dtype], _ptr(out), _ld(out),
                                    _stream(stream))
@@ -280,7 +289,7 @@ def bq_gemm_i8_pertoken_batched(x: torch.Tensor, w: torch.Tensor, deq_scale: tor
         esz = torch.tensor([], dtype=out_dtype).element_size()
         pad = 16 // esz
         ldo = (N + pad - 1) // pad * pad
-        out = torch.empty((B, M, ldo), dtype=out_dtype, device=x.device)[:, :, :N]
+        out = _empty((B, M, ldo), out_dtype, x.device, stream)[:, :, :N]
     ldx, sx = _ld3(x)
     ldw, sw = _ld3(w)
     ldo_, so = _ld3(out)
@@ -298,9 +307,9 @@ def bq_bitlinear_w2a8(x: torch.Tensor, wpacked: torch.Tensor, w_scale: torch.Ten
     """BitLinear forward: act quant into the workspace, ternary integer linear, rescale."""
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = _empty((M, N), out_dtype, x.device, stream)
     nbytes = bq_workspace_bytes(BQ_OP_BITLINEAR_W2A8, M, N, K)
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     st = lib().bq_bitlinear_w2a8(_ptr(x), _DTYPE[x.dtype], M, K, _ptr(wpacked), _ptr(w_scale), N, _ptr(bias),
                                  float(eps), _DTYPE[out.dtype], _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
                                  _stream(stream))
@@ -314,9 +323,9 @@ def bq_linear_w4_grouped(x: torch.Tensor, qweight: torch.Tensor, scales_f16: tor
     M, K = x.shape
     N = qweight.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        out = _empty((M, N), torch.float32, x.device, stream)
     nbytes = bq_workspace_bytes(BQ_OP_LINEAR_W4_GROUPED, M, N, K, group_size)
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     st = lib().bq_linear_w4_grouped(_ptr(x), M, K, _ptr(qweight), _ptr(scales_f16), _ptr(qzeros), _ptr(bias), N,
                                     group_size, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "bq_linear_w4_grouped")
@@ -330,7 +339,7 @@ def bq_bitlinear_w2a8_noalloc(x: torch.Tensor, wpacked: torch.Tensor, w_scale: t
     its scratch in a fixed static device array (see include/bq.h)."""
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = _empty((M, N), out_dtype, x.device, stream)
     st = lib().bq_bitlinear_w2a8_noalloc(_ptr(x), _DTYPE[x.dtype], M, K, _ptr(wpacked), _ptr(w_scale), N, _ptr(bias),
                                          float(eps), _DTYPE[out.dtype], _ptr(out), _stream(stream))
     _check(st, "bq_bitlinear_w2a8_noalloc")
@@ -351,7 +360,7 @@ def bq_weight_quant_int4_pack(w: torch.Tensor, scale_w: torch.Tensor, eps: float
     value or [N]), packed eight per word: int32 [N, K/8]."""
     N, K = w.shape
     if wpacked is None:
-        wpacked = torch.empty((N, K // 8), dtype=torch.int32, device=w.device)
+        wpacked = _empty((N, K // 8), torch.int32, w.device, stream)
     per_channel = 1 if scale_w.numel() == N and N > 1 else 0
     st = lib().bq_weight_quant_int4_pack(_ptr(w), _DTYPE[w.dtype], N, K, _ptr(scale_w), per_channel, float(eps),
                                          _ptr(wpacked), _stream(stream))
@@ -363,7 +372,7 @@ def bq_act_quant_int4(x: torch.Tensor, scale_a: torch.Tensor, eps: float, xq=Non
     """Signed 4-bit codes of x [M,K] (as int8) with step max(scale_a, eps)."""
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        xq = _empty((M, K), torch.int8, x.device, stream)
     st = lib().bq_act_quant_int4(_ptr(x), _DTYPE[x.dtype], M, K, _ld(x), _ptr(scale_a), float(eps), _ptr(xq), _ld(xq),
                                  _stream(stream))
     _check(st, "bq_act_quant_int4")
@@ -375,10 +384,10 @@ def bq_linear_w4a4(x: torch.Tensor, scale_a: torch.Tensor, wpacked: torch.Tensor
     """Forward of the 4-bit activation / 4-bit weight linear with given steps."""
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = _empty((M, N), out_dtype, x.device, stream)
     per_channel = 1 if scale_w.numel() == N and N > 1 else 0
     nbytes = bq_workspace_bytes(BQ_OP_LINEAR_W4A4, M, N, K)
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     st = lib().bq_linear_w4a4(_ptr(x), _DTYPE[x.dtype], M, K, _ptr(scale_a), _ptr(wpacked), _ptr(scale_w),
                               per_channel, N, _ptr(bias), float(eps), _DTYPE[out.dtype], _ptr(out), _ptr(ws),
                               ws.numel() * ws.element_size(), _stream(stream))
@@ -392,11 +401,14 @@ def bq_bitconv1d_weight_pack(w: torch.Tensor, wpacked=None, w_scale=None, worksp
     C_out, Cg, KS = w.shape
     Cgp = (Cg + 63) // 64 * 64
     if wpacked is None:
-        wpacked = torch.empty((KS, C_out, Cgp // 16), dtype=torch.int32, device=w.device)
+        wpacked = _empty((KS, C_out, Cgp // 16), torch.int32, w.device, stream)
     if w_scale is None:
-        w_scale = torch.empty(1, dtype=torch.float32, device=w.device)
-    ws = _workspace(int(lib().bq_bitconv1d_weight_pack_workspace_bytes(C_out, Cg, KS)), w.device, workspace)
-    st = lib().bq_bitconv1d_weight_pack(_ptr(w.contiguous()), _DTYPE[w.dtype], C_out, Cg, KS, _ptr(wpacked),
+        w_scale = _empty(1, torch.float32, w.device, stream)
+    ws = _workspace(int(lib().bq_bitconv1d_weight_pack_workspace_bytes(C_out, Cg, KS)), w.device, workspace, stream)
+    if not w.is_contiguous():
+        with torch.cuda.stream(stream):  # (None: the current one)
+            w = w.contiguous()
+    st = lib().bq_bitconv1d_weight_pack(_ptr(w), _DTYPE[w.dtype], C_out, Cg, KS, _ptr(wpacked),
                                         _ptr(w_scale), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "bq_bitconv1d_weight_pack")
     return wpacked, w_scale
@@ -409,9 +421,9 @@ def bq_bitconv1d(x: torch.Tensor, wpacked: torch.Tensor, w_scale: torch.Tensor, 
     B, C_in, L = x.shape
     L_out = (L + 2 * padding - kernel_size) // stride + 1
     if out is None:
-        out = torch.empty((B, C_out, L_out), dtype=out_dtype, device=x.device)
+        out = _empty((B, C_out, L_out), out_dtype, x.device, stream)
     nbytes = int(lib().bq_bitconv1d_workspace_bytes(B, C_in, L, C_out, kernel_size, stride, padding, groups))
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     st = lib().bq_bitconv1d(_ptr(x), _DTYPE[x.dtype], B, C_in, L, _ptr(ln_weight), _ptr(ln_bias), _ptr(wpacked),
                             _ptr(w_scale), C_out, kernel_size, stride, padding, groups, _ptr(bias), float(eps),
                             _DTYPE[out.dtype], _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -425,11 +437,11 @@ def bq_bitlinear_w2a8_backward(x: torch.Tensor, dout: torch.Tensor, wpacked: tor
     M, K = x.shape
     N = dout.shape[1]
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        dx = _empty((M, K), torch.float32, x.device, stream)
     if dw is None:
-        dw = torch.empty((N, K), dtype=torch.float32, device=x.device)
+        dw = _empty((N, K), torch.float32, x.device, stream)
     nbytes = bq_workspace_bytes(BQ_OP_BITLINEAR_W2A8_BACKWARD, M, N, K)
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     st = lib().bq_bitlinear_w2a8_backward(_ptr(x), _DTYPE[x.dtype], _ptr(dout), M, K, _ptr(wpacked), _ptr(w_scale), N,
                                           float(eps), _ptr(dx), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(),
                                           _stream(stream))
@@ -446,13 +458,13 @@ def bq_linear_w4a4_backward(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor
     N = w.shape[0]
     per_channel = 1 if scale_w.numel() == N and N > 1 else 0
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        dx = _empty((M, K), torch.float32, x.device, stream)
     if dw is None:
-        dw = torch.empty((N, K), dtype=torch.float32, device=x.device)
+        dw = _empty((N, K), torch.float32, x.device, stream)
     if dscale_a is None:
-        dscale_a = torch.empty(1, dtype=torch.float32, device=x.device)
+        dscale_a = _empty(1, torch.float32, x.device, stream)
     nbytes = bq_workspace_bytes(BQ_OP_LINEAR_W4A4_BACKWARD, M, N, K)
-    ws = _workspace(nbytes, x.device, workspace)
+    ws = _workspace(nbytes, x.device, workspace, stream)
     st = lib().bq_linear_w4a4_backward(_ptr(x), _DTYPE[x.dtype], _ptr(w), _ptr(dout), M, K, N, _ptr(scale_a),
                                        _ptr(scale_w), per_channel, float(eps), _ptr(dx), _ptr(dw), _ptr(dscale_a),
                                        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -505,15 +517,6 @@ def _kv4_strides(t: torch.Tensor):
     return (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
-def _kv4_empty(shape, dtype, device, stream):
-    """torch.empty for a call that launches on `stream`: allocated on that stream, so that the caching allocator hands
-    the bytes out again only behind the call's kernels (and takes none that another stream still uses)."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
 def _kv4_call(dev: int, fn, stream, *args):
     """fn(*args, stream handle) with device `dev` current (the library launches on the current device)."""
     if dev == torch.cuda.current_device():
@@ -553,9 +556,9 @@ def bq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Te
     B, ld, width = _kv4_batch(block_table, None, cu_len, starts)
     shape, dev = (total, H, head_dim), cache.get_device()
     if k is None:
-        k = _kv4_empty(shape, out_dtype, cache.device, stream)
+        k = _empty(shape, out_dtype, cache.device, stream)
     if v is None:
-        v = _kv4_empty(shape, k.dtype, cache.device, stream)
+        v = _empty(shape, k.dtype, cache.device, stream)
     if k.shape != shape or v.shape != shape or k.dtype is not v.dtype or k.dtype not in _DTYPE or \
             not (k.is_contiguous() and v.is_contiguous()) or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("k and v must be dense [total, kv_heads, head_dim] of one type on the cache's device")
@@ -585,7 +588,7 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
     pages, pstride, page, H = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
     B, ld, width = _kv4_batch(block_table, seq_lens, cu_q)
     if out is None:
-        out = _kv4_empty((T, Hq, D), q.dtype, q.device, stream)
+        out = _empty((T, Hq, D), q.dtype, q.device, stream)
     elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be dense, of q's shape, type and device")
     if slopes is not None and (slopes.dtype is not torch.float32 or slopes.shape != (Hq,) or
@@ -595,7 +598,7 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
                             not lse.is_contiguous()):
         raise ValueError("lse must be dense fp32 [T, q_heads] on q's device")
     if workspace is None:
-        workspace = _kv4_empty(bq_kv4_attention_workspace_bytes(T, Hq, H, D), torch.uint8, q.device, stream)
+        workspace = _empty(bq_kv4_attention_workspace_bytes(T, Hq, H, D), torch.uint8, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be dense and on q's device")
     qt, qh = _kv4_strides(q)
