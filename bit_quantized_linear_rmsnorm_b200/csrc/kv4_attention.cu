@@ -555,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                     for (int rh = 0; rh < 2; ++rh)
 #pragma unroll
                         for (int r = 0; r < GR; ++r) {
-                            if (!(fabsf(sv[k][rh][r]) <= 65504.0f && fabsf(mv[k][rh][r]) <= 65504.0f)) {
+                            // (mv is m + 8 s: up to 9 x 65504 of what is stored as finite)
+                            if (!(fabsf(sv[k][rh][r]) <= 65504.0f && fabsf(mv[k][rh][r]) <= 9.0f * 65504.0f)) {
                                 sv[k][rh][r] = mv[k][rh][r] = 0.0f;
                                 spoilt |= 1u << (4 * k + 2 * rh + r);
                             }

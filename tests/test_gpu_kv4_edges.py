@@ -96,6 +96,24 @@ def test_many_rows_without_a_place_and_empty_slots(D, G, kw):
     run_attention(s, query(s, 8, 4, "bf16"), [4, 4], **kw)
 
 
+# ------------------------------------------------------------------ values beyond fp16
+@pytest.mark.parametrize("low,high", [(60000, 75000), (65504, 3e5), (-6e4, 1e6), (-1e6, -65600), (7e4, 7e4)])
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_values_whose_middle_leaves_fp16(D, G, low, high):
+    """What the write stores of bf16 values beyond fp16 is finite (minimum and step are), and so is what is attended to,
+    in either kernel, alone or beside ordinary tokens."""
+    for kind in ("all", "some"):
+        s = Setup([150], 2, D, G, 16, seed=27)
+        for p in range(150):
+            k, v = s.rng.standard_normal((2, 2, D)).astype(np.float32)
+            if kind == "all" or p % 40 == 3:
+                v = s.rng.uniform(low, high, (2, D)).astype(np.float32)
+            s.host.put(*s.place(0, p), k, v)
+        for n in (1, 4, 40):
+            out = run_attention(s, query(s, n, 4, "bf16"), [n])
+            assert out.isfinite().all()
+
+
 # ------------------------------------------------------------------ positions at the ends of their range
 def test_positions_near_the_end_of_32_bits():
     """A table as wide as positions go (2^24 pages of 128).  Up to 2^31 - 65537 a row is attended to as anywhere else;
