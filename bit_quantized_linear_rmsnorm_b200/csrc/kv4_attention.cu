@@ -26,8 +26,8 @@
 // the type of the instruction; the sums that go with it (the divisor, and
 // the minima's term) are taken of the same rounded weights, so the rounding
 // acts as a relative error of a weight, 2^-11 at most, and cancels for a
-// single token.  (A step far below the others' would leave fp16's range with
-// its weight: such a token counts in the sums with its weight as it is.)
+// single token.  (A step far below the others' can leave fp16's normal range
+// with its weight: such a weight counts in the sums as it is.)
 // Running maximum, sums and products are fp32.  The maximum is
 // that of z + log2 s_v, which keeps p * s_v within fp16 whatever the steps
 // are; it is raised only when a score passes it by 2^8 (the weights then stay
@@ -522,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
             }
 
             // ---- tokens that need care: values that are not finite count only for the rows that see them, and a step
-            // far below the others' would lose p * s_v to fp16's underflow, so such a token's weight goes into the
-            // sums as it is (bits 2 (2 k + rh) + group)
+            // far below the others' may lose p * s_v to fp16's underflow, so such a token's weight goes into the
+            // sums apart (bits 2 (2 k + rh) + group)
             uint32_t direct = 0, spoilt = 0;
             float lv[2][2];  // log2 of the step, for the maximum
 #pragma unroll
@@ -677,8 +677,12 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
 #pragma unroll
                                 for (int cc = 0; cc < 2; ++cc) {
                                     const float x = z[k][nb][2 * rh + cc], e = ex2(x - (m[nb][cc] - kLift));
-                                    l[nb][cc][r] += e;
-                                    mo[nb][cc][r] = fmaf(e, mv[k][rh][r], mo[nb][cc][r]);
+                                    // (rounded as in the products, for a row to which the step is not small at all;
+                                    // as it is below fp16's normal numbers)
+                                    const float ps = unpack_f16(pack_f16(e * sv[k][rh][r], 0.0f)).x;
+                                    const float w = ps >= 6.103515625e-05f ? ps * rcp(sv[k][rh][r]) : e;
+                                    l[nb][cc][r] += w;
+                                    mo[nb][cc][r] = fmaf(w, mv[k][rh][r], mo[nb][cc][r]);
                                     // NaN for the rows that see it
                                     if (((spoilt >> (4 * k + 2 * rh + r)) & 1u) && x > -INFINITY)
                                         mo[nb][cc][r] = __int_as_float(0x7fffffff);

@@ -41,6 +41,20 @@ def check_lse(s, lse, q, cu, scale, **kw):
     assert not bad.any()
 
 
+def check_rounded(s, out, q, cu, scale, **kw):
+    """check_attention, but where the value itself, to within its bound, is not below 65520 an fp16 output is an infinity
+    of its sign: 65520 lies half-way between 65504, the largest fp16, and the 2^16 that would follow, and rounds up."""
+    want, _, tol = ref.attention(q.double().cpu().numpy(), s.host, s.table, s.lens, cu, scale, **kw)
+    over = (np.abs(want) + tol >= 65520) & (out.dtype is torch.float16)
+    got = out.double().cpu().numpy()
+    held = np.where(over & np.isinf(got) & (np.sign(got) == np.sign(want)), want, got)
+    info = torch.finfo(out.dtype)
+    bound = tol + (info.eps / 2) * (np.abs(want) + tol) + info.smallest_normal * info.eps
+    assert np.array_equal(np.isnan(held), np.isnan(want))
+    ok = np.isnan(want) | (np.abs(held - want) <= bound)
+    assert ok.all(), (np.argwhere(~ok)[:5], np.nanmax(np.abs(held - want) / bound))
+
+
 # ------------------------------------------------------------------ rows that see nothing of a tile, or nothing at all
 @pytest.mark.parametrize("size", [1e-30, 1e-3, 0.006, 300.0])
 @pytest.mark.parametrize("D,G", SHAPES)
@@ -112,6 +126,40 @@ def test_values_whose_middle_leaves_fp16(D, G, low, high):
         for n in (1, 4, 40):
             out = run_attention(s, query(s, n, 4, "bf16"), [n])
             assert out.isfinite().all()
+
+
+# ------------------------------------------------------------------ values of very different sizes
+@pytest.mark.parametrize("counts", [[1, 1], [2, 5]])
+@pytest.mark.parametrize("kind", ["larger", "offset", "first", "small", "not finite"])
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_values_beside_far_larger_ones(D, G, kind, counts):
+    """Tokens that a row does not see, or hardly weighs, and whose values are far larger than those that it does: in the
+    same tile or in an earlier one, by their steps or by their minima only."""
+    s = Setup([333, 81], 2, D, G, 64, seed=29)
+    for b, n in enumerate(s.lens):
+        for t in range(n):
+            k, v = s.rng.standard_normal((2, 2, D)).astype(np.float32)
+            far = t % 11 == 4
+            if kind == "larger" and far:
+                v *= 1.5e4
+            elif kind == "offset" and far:
+                v += 3e4
+            elif kind == "first":
+                v *= 1.0 if t >= 64 else 2e4
+            elif kind == "small":
+                v *= 1.5e4 if far else 2.0 ** -6
+            elif kind == "not finite" and far:
+                v *= 1.5e4 if t % 2 else np.nan
+            if far:
+                k[:] = 0
+            s.host.put(*s.place(b, t), k, v)
+    for dtype in ("f16", "bf16"):
+        q = query(s, sum(counts), 4, dtype, scale=4.0)
+        for window in (1, 9, 130):
+            out = bq.bq_kv4_attention(q, s.cuda(), dev(s.table), dev(s.lens), G, cu_q=dev(offsets(counts)), max_q=max(counts),
+                                      window=window)
+            check_rounded(s, out, q, offsets(counts), D ** -0.5, window=window)
+    status_ok()
 
 
 # ------------------------------------------------------------------ positions at the ends of their range
