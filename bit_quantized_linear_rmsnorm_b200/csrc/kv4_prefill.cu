@@ -12,7 +12,10 @@
 // so that the output is (2^e0 O + 2^e1 L_m) / L_1: the divisor and the middles'
 // term are sums of the same rounded weights w as the codes' term, and the
 // rounding of a weight (2^-11 at most) changes how much a token counts, never
-// what it stands for.  1/mu and the middles are pairs of fp16 (22 bits).  The
+// what it stands for.  1/mu is a pair of fp16 (22 bits); so is a middle, whose
+// second half is held times 2^14, so that one far below the largest keeps its
+// bits (to 2^-41 of the largest; 2^-27 without that, which a row that sees only
+// small ones would notice).  The
 // values' codes are taken from the middle because the tensor core's additions
 // round toward zero: sums of 0..15 drift with every step, and what is left of
 // them after the minima's term is small (0.0029 against 0.0017 relative error
@@ -66,6 +69,7 @@ constexpr int kCols = 256;     // columns of an item
 constexpr int kPThreads = 768;
 constexpr int kLaunchRegs = 80, kSoftmaxRegs = 88, kOtherRegs = 64;  // registers: 512 x 88 + 256 x 64 = 768 x 80
 constexpr int kRing = 3;       // raw stages
+constexpr float kRest = 16384.0f;  // the second half of a middle is held times this
 constexpr float kRise = 7.0f;  // the running maximum is raised when passed by more
 constexpr int kOverhead = 192; // cost of starting an item, in tokens (8 ragged prompts: 236, 222, 228, 249 us at 96, 192, 400, 800)
 
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 tmem_ld_32x32b_x16(ot + grp * (G + 16) + G, l);
                 tmem_wait_ld();
                 float den = __uint_as_float(l[0]) + __uint_as_float(l[1]), row_sum = row.sum;
-                const float lm = (__uint_as_float(l[2]) + __uint_as_float(l[3])) * w1;
+                const float lm = fmaf(__uint_as_float(l[3]), 1.0f / kRest, __uint_as_float(l[2])) * w1;
                 if (a.lse == nullptr) row_sum = den;
                 if (spoilt) den = row_sum = __int_as_float(0x7fffffff);
                 const float inv = !g.whole ? 1.0f : den == 0.0f ? 0.0f : __fdividef(1.0f, den);
@@ -978,7 +982,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                                 mu = x.x * pow2i(-k - e0);
                                 inv = rcp(mu);
                                 lm = fmaf(8.0f, x.x, x.y) * pow2i(-e1);
-                                if (fabsf(inv) <= 32768.0f && fabsf(lm * inv) <= 32768.0f) {
+                                if (fabsf(inv) <= 32768.0f && fabsf(lm * inv) <= 8192.0f) {
                                     lm *= inv;
                                     const float b = pow2i(k);
                                     mult = pack_f16(b, b);
@@ -998,9 +1002,12 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                             }
                         }
                         sts32f(par + ((2 * GR + r) * TOK + tok) * 4, mu);
+                        // A middle is at most 2^13 here (1 / mu at most 2^9), so what fp16 leaves of it, times kRest,
+                        // is at most 2^15, and the pair holds it to 2^-39: to 2^-41 of the largest middle of the part,
+                        // whoever sees the token that has that one.
                         const uint32_t hi = pack_f16(inv, lm);
                         const float2 h = unpack_f16(hi);
-                        const uint32_t lo = pack_f16(inv - h.x, lm - h.y);
+                        const uint32_t lo = pack_f16(inv - h.x, (lm - h.y) * kRest);
                         sts128(vb + (G / 8) * (TOK * 16), __byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632), 0, 0);
                         if (warp == 16 && lane == 0) s_info[buf] = {e0, e1, odd ? 1 : 0};
                     }

@@ -129,7 +129,7 @@ def test_values_whose_middle_leaves_fp16(D, G, low, high):
 
 
 # ------------------------------------------------------------------ values of very different sizes
-@pytest.mark.parametrize("counts", [[1, 1], [2, 5]])
+@pytest.mark.parametrize("counts", [[1, 1], [2, 5], [100, 70]])
 @pytest.mark.parametrize("kind", ["larger", "offset", "first", "small", "not finite"])
 @pytest.mark.parametrize("D,G", SHAPES)
 def test_values_beside_far_larger_ones(D, G, kind, counts):
