@@ -113,7 +113,7 @@ struct SeqPlan {
     int64_t first;  // first row
     int rows;       // rows computed (at most max_q)
     int pos0;       // position of the first row
-    int hi;         // last position that is read, or -1
+    int lo, hi;     // first and last position that a row sees (hi -1: none)
     int t0, tiles;  // first tile and number of tiles (1 for rows that see nothing)
     int blocks;     // column blocks
 };
@@ -128,9 +128,9 @@ __device__ __forceinline__ SeqPlan plan_seq(const Kv4AttnArgs &a, int b, int sha
     p.pos0 = static_cast<int>(max(static_cast<int64_t>(len) - n, static_cast<int64_t>(-0x7fffffff)));
     const int cap = kv4_capacity(a.pool);
     p.hi = static_cast<int>(min(static_cast<int64_t>(p.pos0) + p.rows, static_cast<int64_t>(cap))) - 1;
-    const int lo = a.window > 0 ? static_cast<int>(max(static_cast<int64_t>(p.pos0) - a.window + 1, int64_t(0))) : 0;
-    if (p.hi < lo) p.hi = -1;
-    p.t0 = lo / kTile;
+    p.lo = a.window > 0 ? static_cast<int>(max(static_cast<int64_t>(p.pos0) - a.window + 1, int64_t(0))) : 0;
+    if (p.hi < p.lo) p.hi = -1;
+    p.t0 = p.lo / kTile;
     p.tiles = p.hi < 0 ? 1 : p.hi / kTile - p.t0 + 1;
     p.blocks = static_cast<int>((static_cast<int64_t>(p.rows) * share + cols - 1) / cols);
     return p;
@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                     return static_cast<int64_t>(pg) * a.pool.page_stride +
                            static_cast<int64_t>(head) * a.pool.block_bytes;
                 };
-                if (tok <= p.hi) src0 = page_at(tok);
+                // (a page that ends before the window may be gone, and its entry name none)
+                if (tok <= p.hi && (page_log2 != 4 || tok + 16 > p.lo)) src0 = page_at(tok);
                 if (page_log2 == 4 && tok + 16 <= p.hi) src1 = page_at(tok + 16);
             }
         };
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
 #pragma unroll
                     for (int rh = 0; rh < 2; ++rh) {
                         const int tok = 16 * k + gt + 8 * rh;
-                        if (gone || tok0 + tok > p.hi) {  // a place that holds nothing
+                        if (gone || tok0 + tok > p.hi || tok0 + tok < p.lo) {  // a place that holds nothing for these rows
 #pragma unroll
                             for (int r = 0; r < GR; ++r) {
                                 sv[k][rh][r] = fmaxf(step_ref, 5.9604644775390625e-08f);

@@ -162,6 +162,35 @@ def test_values_beside_far_larger_ones(D, G, kind, counts):
     status_ok()
 
 
+# ------------------------------------------------------------------ pages behind a window
+@pytest.mark.parametrize("kw", [dict(window=1), dict(window=16), dict(window=50, slopes=1), dict(window=17, softcap=9.0)])
+@pytest.mark.parametrize("D,G", SHAPES)
+@pytest.mark.parametrize("page", [16, 32, 64])
+def test_pages_before_the_window_may_be_gone(page, D, G, kw):
+    """Entries of pages that no row of the call reaches any more name no page: nothing is reported, and nothing of what
+    lies there, or of what an earlier tile left in shared memory, counts."""
+    kw = extras(kw, 4)
+    lens = [1, 17, 40, 81, 200, 333]
+    for counts in ([1] * 6, [1, 2, 5, 3, 6, 4], [1, 10, 40, 30, 100, 33]):
+        s = Setup(lens, 2, D, G, page, seed=28)
+        for b, n in enumerate(lens):
+            first = max(n - counts[b] - kw["window"] + 1, 0)  # the first position that a row sees
+            for t in range(n):
+                k, v = s.rng.standard_normal((2, 2, D)).astype(np.float32)
+                # far larger than the rest, then not finite, where no row looks
+                s.host.put(*s.place(b, t), k, v if t >= first else v * (3e4 if t % 3 else np.nan))
+        pool = s.cuda()
+        out = run_attention(s, query(s, sum(counts), 4, "bf16"), counts, **kw)
+        full, q = s.table.copy(), query(s, sum(counts), 4, "bf16")
+        want = bq.bq_kv4_attention(q, pool, dev(full), dev(lens), G, cu_q=dev(offsets(counts)), max_q=max(counts), window=kw["window"])
+        for b, n in enumerate(lens):
+            first = max(n - counts[b] - kw["window"] + 1, 0)
+            s.table[b, : first // page] = -1
+        got = bq.bq_kv4_attention(q, pool, dev(s.table), dev(lens), G, cu_q=dev(offsets(counts)), max_q=max(counts), window=kw["window"])
+        assert torch.equal(got, want) and out.isfinite().all()
+        status_ok()
+
+
 # ------------------------------------------------------------------ positions at the ends of their range
 def test_positions_near_the_end_of_32_bits():
     """A table as wide as positions go (2^24 pages of 128).  Up to 2^31 - 65537 a row is attended to as anywhere else;
