@@ -121,11 +121,10 @@ __device__ __forceinline__ SeqPlan plan_seq(const Kv4AttnArgs &a, int b, int sha
     SeqPlan p;
     int n;
     kv4_rows(a.seqs, b, p.first, n);
-    const int len = __ldg(a.seqs.lens + b);
     // (a row past the tensor is never touched, whatever the offsets say)
     p.rows = static_cast<int>(min(static_cast<int64_t>(min(n, a.max_q)), a.total - p.first));
     if (n <= 0 || p.rows < 0 || p.first < 0) p.rows = 0;
-    p.pos0 = static_cast<int>(max(static_cast<int64_t>(len) - n, static_cast<int64_t>(-0x7fffffff)));
+    p.pos0 = kv4_first_position(a.seqs, b, n);
     const int cap = kv4_capacity(a.pool);
     p.hi = static_cast<int>(min(static_cast<int64_t>(p.pos0) + p.rows, static_cast<int64_t>(cap))) - 1;
     p.lo = a.window > 0 ? static_cast<int>(max(static_cast<int64_t>(p.pos0) - a.window + 1, int64_t(0))) : 0;

@@ -42,6 +42,13 @@ __device__ __forceinline__ void kv4_rows(const Kv4Seqs &s, int b, int64_t &first
     }
 }
 
+// Position of the first of n rows of sequence b.  A length below 0 holds as
+// few tokens as 0 does: with no less than -n, the distance from any row to any
+// token has 32 bits.
+__device__ __forceinline__ int kv4_first_position(const Kv4Seqs &s, int b, int n) {
+    return max(__ldg(s.lens + b), 0) - max(n, 0);
+}
+
 // Positions that attention reaches: those of the table, and no more than leave
 // room above them, so that the first token of a tile, of a copy, or of a page
 // looked up ahead is a 32-bit number for every tile that begins below.

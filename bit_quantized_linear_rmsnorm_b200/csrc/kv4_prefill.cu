@@ -284,7 +284,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int sha
     kv4_rows(a.seqs, b, w.first, n);
     w.rows = static_cast<int>(min(static_cast<int64_t>(min(n, a.max_q)), a.total - w.first));
     if (n <= 0 || w.rows < 0 || w.first < 0) w.rows = 0;
-    w.pos0 = static_cast<int>(max(static_cast<int64_t>(__ldg(a.seqs.lens + b)) - n, int64_t(-0x7fffffff)));
+    w.pos0 = kv4_first_position(a.seqs, b, n);
     w.cap = kv4_capacity(a.pool);
     w.step = max(kCols / share, 1);
     w.a0 = w.pos0 + w.step;

@@ -500,7 +500,7 @@ bq_status bq_bitlinear_w2a8_noalloc(const void *x, bq_dtype x_dtype, int64_t M, 
  *   seq_lens: int32 [batch], tokens of the sequence in the cache including
  *     the call's rows, so that row j of n stands at position
  *     seq_lens[b] - n + j.  A row whose position is negative has no place: it
- *     is not written, and attends to nothing.
+ *     is not written, and attends to nothing.  (A negative length is like 0.)
  *   total, batch: rows in all and sequences; total == 0 or batch == 0 is a
  *     valid empty call.
  * Tables, lengths and offsets are read on the device: a captured call can be

@@ -241,3 +241,25 @@ def test_calls_that_overlap_on_streams_given_to_them(n):
             assert torch.equal(got[i], want[i]) and (other[i] == 7).all()
             assert torch.equal(reads[i][0], kv[0]) and torch.equal(reads[i][1], kv[1])
     status_ok()
+
+
+@pytest.mark.parametrize("kw", EXTRAS)
+@pytest.mark.parametrize("n", [1, 40])
+def test_lengths_below_zero_hold_nothing(n, kw):
+    """Any negative length is like 0, down to -2^31: 0 and -inf, nothing reported; the others are as they would be."""
+    kw = extras(kw, 4)
+    s = Setup([90, 0, 0, 0, 50], 2, 64, 64, 16, seed=30).fill()
+    q = query(s, 5 * n, 4, "bf16")
+    want = run_attention(s, q, [n] * 5, **kw)
+    slopes = None if "slopes" not in kw else dev(kw["slopes"], torch.float32)
+    lse = torch.zeros(5 * n, 4, device="cuda")
+    out = bq.bq_kv4_attention(q, s.cuda(), dev(s.table), dev([90, -1, -2 ** 31, -2 ** 31 + 30, 50]), 64, lse=lse,
+                              window=kw.get("window", 0), softcap=kw.get("softcap", 0.0), slopes=slopes)
+    assert torch.equal(out, want) and not out[n:4 * n].any()
+    assert lse[n:4 * n].isneginf().all() and lse[n - 1].isfinite().all()
+    pool = s.cuda()
+    kv = torch.randn(5, 2, 64, device="cuda").bfloat16()
+    for lens in ([-1] * 5, [-2 ** 31] * 5):
+        bq.bq_kv4_write(kv, kv, pool, dev(s.table), dev(lens), 64)
+    assert torch.equal(pool, s.cuda())
+    status_ok()
