@@ -900,7 +900,9 @@ bq_status bq_kv4_attention(const void *q, bq_dtype dtype, int64_t total, int64_t
     a.q_heads = static_cast<int>(q_heads);
     a.max_q = cu_q == nullptr ? a.seqs.uniform_n : static_cast<int>(max_q < total ? max_q : total);
     a.scale = scale;
-    a.softcap = softcap;
+    // (a cap of 2^96 moves no score below 2^83 by half a step of fp32)
+    a.softcap = softcap < 0x1p96f ? softcap : 0.0f;
+    a.cap_rate = a.softcap > 0.0f ? std::fmin(2.8853900817779268f / a.softcap, 3.402823466e38f) : 0.0f;
     a.window = window > kMaxDim ? 0 : static_cast<int>(window);  // (no sequence is longer)
     a.slopes = slopes;
     a.out = out;

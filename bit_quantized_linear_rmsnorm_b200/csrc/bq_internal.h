@@ -260,6 +260,7 @@ struct Kv4AttnArgs {
     int q_heads = 0;
     int max_q = 0;  // most rows of one sequence
     float scale = 0.0f, softcap = 0.0f;
+    float cap_rate = 0.0f;  // 2 log2(e) / softcap
     int window = 0;
     const float *slopes = nullptr;
     void *out = nullptr;  // [total][q_heads][head_dim]

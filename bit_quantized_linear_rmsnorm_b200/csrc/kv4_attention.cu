@@ -135,7 +135,7 @@ __device__ __forceinline__ SeqPlan plan_seq(const Kv4AttnArgs &a, int b, int sha
     return p;
 }
 
-template <typename C, bool MODS, typename T>
+template <typename C, Mods MODS, typename T>
 __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4AttnArgs a, const Kv4Ws ws, uint32_t *status) {
     constexpr int D = C::D, NB = C::NB, HV = C::HV, GR = C::GR;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                 k = min(k, 120);
                 const float up = finite ? __uint_as_float(static_cast<uint32_t>(127 + k) << 23) : 0.0f;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                const float zs = a.scale * (MODS ? 1.0f : 1.4426950408889634f) * down;
+                const float zs = a.scale * (MODS != kPlain ? 1.0f : 1.4426950408889634f) * down;
                 fc[nb] = zs * 16777216.0f;
 #pragma unroll
                 for (int r = 0; r < GR; ++r) sc[nb][r] = 0.0f;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                     const int c = nb * 8 + 2 * t + cc;
                     pos[nb][cc] = c < ncols ? p.pos0 + (col0 + c) / share : -1;
                     slope[nb][cc] = 0.0f;
-                    if (MODS && a.slopes != nullptr && c < ncols)
+                    if (MODS != kPlain && a.slopes != nullptr && c < ncols)
                         slope[nb][cc] = __ldg(a.slopes + head * share + (col0 + c) % share);
                 }
             }
@@ -481,10 +481,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
                                 y = fmaf(km[1], sq[nb][cc][1], km[0] * sq[nb][cc][0]);
                             }
                             x = fmaf(x, f[nb][cc], y);
-                            if constexpr (MODS) {
-                                if (a.softcap > 0.0f)  // cap * tanh(x / cap) = cap * (1 - 2 / (exp(2 x / cap) + 1))
-                                    x = a.softcap - 2.0f * a.softcap *
-                                                        rcp(ex2(x * (2.8853900817779268f / a.softcap)) + 1.0f);
+                            if constexpr (MODS != kPlain) {
+                                if (a.softcap > 0.0f) {
+                                    const float v = x * a.cap_rate;
+                                    x = fmaf(-2.0f * a.softcap, rcp(ex2(v) + 1.0f), a.softcap);
+                                    if (MODS == kFarMods && fabsf(v) < kSeries)
+                                        x = cap_series(v, a.softcap * (0.5f / 1.4426950408889634f));
+                                }
                                 x = fmaf(slope[nb][cc], static_cast<float>(tok0 + tok - pos[nb][cc]), x);
                                 x *= 1.4426950408889634f;
                             }
@@ -806,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) kv4_decode_kernel(const Kv4
     }
 }
 
-template <typename C, bool MODS, typename T>
+template <typename C, Mods MODS, typename T>
 cudaError_t launch_decode(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {
     auto kern = kv4_decode_kernel<C, MODS, T>;
     static SmemOptIn opt_in;
@@ -832,10 +835,11 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t s, const Dev
         using T = decltype(tag);
         constexpr int D = decltype(shape)::D, G = decltype(shape)::G;
         const int64_t cols = static_cast<int64_t>(a.max_q) * (a.q_heads / a.pool.kv_heads);
-        const bool mods = a.softcap > 0.0f || a.slopes != nullptr;
+        const Mods mods = mods_of(a);
         auto go = [&](auto c) {
             using C = decltype(c);
-            return mods ? launch_decode<C, true, T>(a, s, dev) : launch_decode<C, false, T>(a, s, dev);
+            if (mods == kPlain) return launch_decode<C, kPlain, T>(a, s, dev);
+            return mods == kNearMods ? launch_decode<C, kNearMods, T>(a, s, dev) : launch_decode<C, kFarMods, T>(a, s, dev);
         };
         if (cols > kKv4FewColumns) return launch_kv4_prefill(a, s, dev);
         if (cols <= 8) return go(Shape<D, G, 1>());

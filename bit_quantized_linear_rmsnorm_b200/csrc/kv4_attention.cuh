@@ -30,6 +30,27 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Capped scores, cap tanh(x / cap), from v = 2 log2(e) x / cap.  cap (1 - 2 /
+// (2^v + 1)) is off by cap 2^-22 (exponential, reciprocal): 2^-16 at kFarCap, a
+// 30th of a weight's own rounding.  Beyond it that would grow with the cap, so
+// where |x / cap| < 1/4 the first terms of tanh's power series take its place:
+// off by 2^-21 of the score; the other form is by 2^-20 there.
+// (A variant of its own: in one with small caps and biases its registers cost
+// prompts with a bias 4% of their time, one token with a cap of 30 3%; itself
+// it takes 858 us for 2048 rows after 8192, where a cap of 30 takes 767.)
+constexpr float kFarCap = 64.0f;
+enum Mods { kPlain, kNearMods, kFarMods };  // nothing beside the products; a cap up to kFarCap, a bias, or both; a cap beyond
+inline Mods mods_of(const Kv4AttnArgs &a) {
+    return a.softcap > kFarCap ? kFarMods : a.softcap > 0.0f || a.slopes != nullptr ? kNearMods : kPlain;
+}
+constexpr float kSeries = 0.72134752044448170f;  // v at x / cap = 1/4
+__device__ __forceinline__ float cap_series(float v, float scale) {  // scale v (1 - u^2 / 3 + 2 u^4 / 15 - 17 u^6 / 315)
+    constexpr float k = 1.0f / (2.8853900817779268f * 2.8853900817779268f);  // u^2 = k v^2
+    const float s = v * v;
+    const float p = fmaf(s, fmaf(s, -17.0f / 315.0f * k * k * k, 2.0f / 15.0f * k * k), -1.0f / 3.0f * k);
+    return fmaf(scale * v, s * p, scale * v);
+}
+
 // {lo, hi} as a pair of fp16
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;

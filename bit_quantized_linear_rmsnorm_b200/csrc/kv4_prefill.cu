@@ -377,7 +377,7 @@ enum Bar {
     kBars = DRAIN + 1
 };
 
-template <typename C, bool MODS, typename T>
+template <typename C, Mods MODS, typename T>
 __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4AttnArgs a, const Kv4Ws ws, uint32_t *status) {
     constexpr int D = C::D, GR = C::GR, G = C::G, TOK = C::TOK, SC = C::SC, OC = C::OC;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
                 // codes are c 2^-24; (not 0: a hidden score is -inf before it meets this factor, and stays that)
                 float f = fmaxf(fabsf(a.scale) * 1.4426950408889634f * down * 16777216.0f, 7.8886090522101181e-31f);
-                if (MODS && a.softcap > 0.0f) f *= 2.0f / a.softcap;  // the argument of tanh, times 2 log2(e)
+                if (MODS != kPlain && a.softcap > 0.0f) f = fminf(f * 2.0f / a.softcap, 3.402823466e38f);  // to tanh's argument, times 2 log2(e)
                 const uint32_t dst = base + C::OFF_Q + tile * C::QB + part * (D / 16) * (kRows * 16) + row * 16;
                 float sq = 0.0f;
 #pragma unroll
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 const float other = __shfl_xor_sync(0xffffffffu, sq, 1);
                 if (part == 0) {
                     float slope = 0.0f;
-                    if (MODS && a.slopes != nullptr && on)
+                    if (MODS != kPlain && a.slopes != nullptr && on)
                         slope = __ldg(a.slopes + g.head * share + hh) * 1.4426950408889634f;
                     s_rows[c] = {f, {GR == 1 ? sq + other : sq, other}, slope, on ? g.pos0 + qrow : -1, finite ? 1 : 0, 0.0f, 0.0f};
                 }
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 f[i] = rows[8 * i].f;
 #pragma unroll
                 for (int r = 0; r < GR; ++r) sq[i][r] = rows[8 * i].sq[r];
-                slope2[i] = MODS ? rows[8 * i].slope : 0.0f;
+                slope2[i] = MODS != kPlain ? rows[8 * i].slope : 0.0f;
                 pos[i] = rows[8 * i].pos;
                 m[i] = kNoMax;
                 sum[i] = 0.0f;
@@ -640,14 +640,25 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                 }
                 const uint32_t mu = par + (2 * GR * TOK + 2 * t4) * 4;
 
-                if constexpr (MODS) {  // scores in powers of two from here on
+                if constexpr (MODS != kPlain) {  // scores in powers of two from here on
                     const float cap2 = a.softcap * 1.4426950408889634f;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint64_t f2 = pack64(f[i], f[i]), slopes = pack64(slope2[i], slope2[i]);
                         const float away = static_cast<float>(tok0 + 2 * t4 - pos[i]);
                         const uint64_t bias = pack64(slope2[i] * away, slope2[i] * (away + 1.0f));
-                        if (a.softcap > 0.0f) {  // cap tanh(x) = cap (1 - 2 / (exp(2 x) + 1))
+                        if (MODS == kFarMods) {
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                const float2 v = unpack64(mul2(y[b][i], f2));
+                                const float2 d = unpack64(fma2(slopes, pack64(8.0f * b, 8.0f * b), bias));
+                                float2 z = make_float2(fmaf(-2.0f * cap2, rcp(ex2(v.x) + 1.0f), cap2),
+                                                       fmaf(-2.0f * cap2, rcp(ex2(v.y) + 1.0f), cap2));
+                                if (fabsf(v.x) < kSeries) z.x = cap_series(v.x, 0.5f * a.softcap);
+                                if (fabsf(v.y) < kSeries) z.y = cap_series(v.y, 0.5f * a.softcap);
+                                y[b][i] = pack64(z.x + d.x, z.y + d.y);
+                            }
+                        } else if (a.softcap > 0.0f) {
 #pragma unroll
                             for (int b = 0; b < NB; ++b) {
                                 const float2 z = unpack64(mul2(y[b][i], f2));
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         const float2 z = unpack64(y[b][i]);
                         top[i] = fmaxf(top[i], fmaxf(z.x, z.y));
                     }
-                    if (!MODS) top[i] *= f[i];
+                    if (MODS == kPlain) top[i] *= f[i];
                     rise |= top[i] > m[i] + kRise;
                 }
                 if (__any_sync(0xffffffffu, rise) || (j > 0 && (info.e0 != e0 || info.e1 != e1))) {
@@ -727,7 +738,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
 
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float f1 = MODS ? 1.0f : f[i];
+                    const float f1 = MODS != kPlain ? 1.0f : f[i];
                     const uint64_t f2 = pack64(f1, f1), off2 = pack64(kLift - m[i], kLift - m[i]);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
@@ -1192,7 +1203,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
     if (warp == 22) tmem_dealloc(s_tmem, 512);
 }
 
-template <typename C, bool MODS, typename T>
+template <typename C, Mods MODS, typename T>
 cudaError_t launch_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {
     auto kern = kv4_prefill_kernel<C, MODS, T>;
     static SmemOptIn opt_in;
@@ -1216,10 +1227,11 @@ cudaError_t launch_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &
 cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev) {
     auto by_shape = [&](auto tag) {
         using T = decltype(tag);
-        const bool mods = a.softcap > 0.0f || a.slopes != nullptr;
+        const Mods mods = mods_of(a);
         auto go = [&](auto c) {
             using C = decltype(c);
-            return mods ? launch_prefill<C, true, T>(a, s, dev) : launch_prefill<C, false, T>(a, s, dev);
+            if (mods == kPlain) return launch_prefill<C, kPlain, T>(a, s, dev);
+            return mods == kNearMods ? launch_prefill<C, kNearMods, T>(a, s, dev) : launch_prefill<C, kFarMods, T>(a, s, dev);
         };
         if (a.pool.head_dim == 64) return go(PShape<64, 64>());
         return a.pool.group_size == 64 ? go(PShape<128, 64>()) : go(PShape<128, 128>());

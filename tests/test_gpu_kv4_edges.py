@@ -263,3 +263,33 @@ def test_lengths_below_zero_hold_nothing(n, kw):
         bq.bq_kv4_write(kv, kv, pool, dev(s.table), dev(lens), 64)
     assert torch.equal(pool, s.cuda())
     status_ok()
+
+
+# ------------------------------------------------------------------ caps of every size
+@pytest.mark.parametrize("n", [1, 5, 60])
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_caps_of_every_size(D, G, n):
+    """A cap costs a score no more than 2^-20 of its size, however large the cap; the smallest ones work as well."""
+    s = Setup([150, 40], 2, D, G, 32, seed=31).fill()
+    q = query(s, 2 * n, 4, "f16", scale=1.5)
+    cu, scale = offsets([n, n]), D ** -0.5
+    q64 = q.double().cpu().numpy()
+    _, _, free = ref.attention(q64, s.host, s.table, s.lens, cu, scale)  # the bound without a cap
+    biggest = np.abs(s.host.values(1, s.table[0], 150)).max()
+    zmax = max(np.abs(scale * np.einsum("thd,khd->thk", q64[b * n:(b + 1) * n], np.repeat(
+        s.host.values(0, s.table[b], s.lens[b]), 2, axis=1))).max() for b in range(2))
+    for cap in (63.0, 65.0, 300.0, 1e4, 1e5, 1e6, 1e7, 1e20, 1e28, 1e29, 1e35, 3e38):
+        out = bq.bq_kv4_attention(q, s.cuda(), dev(s.table), dev(s.lens), G, softcap=cap)
+        want = ref.attention(q64, s.host, s.table, s.lens, cu, scale, softcap=cap)[0]
+        # zmax <= cap / 4 or so: a weight moves by twice its score's error at most, the output by that times |v - out|;
+        # up to the border of the two forms the error is the cap's, 2^-22 of it.  The softmax itself moves by less than
+        # 3 (zmax / cap)^2 zmax from the free one, whose bound is scaled by that.
+        dz = max(2.0 ** -20 * zmax, 2.0 ** -22 * 64)
+        tol = free * (1 + 2 * zmax ** 3 / cap ** 2) + 2 * dz * 2 * biggest
+        got = out.double().cpu().numpy()
+        assert (np.abs(got - want) <= tol + 2.0 ** -11 * (np.abs(want) + tol) + 2.0 ** -24).all(), cap
+    for cap in (1e-3, 1e-30, 1e-40, 4.0):
+        run_attention(s, q, [n, n], softcap=cap)
+    for cap in (64.0, 200.0):  # with what else changes a score
+        run_attention(s, q, [n, n], softcap=cap, slopes=2.0 ** -np.arange(1.0, 5.0), window=33)
+    status_ok()
