@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import os
+import re
 import shutil
 import subprocess
 
@@ -47,12 +48,46 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+# Kernels whose warps share out (setmaxnreg) the registers that a CTA is launched with: more than that and they wait for
+# ever, so each variant has to be compiled to the very count that the source's constant names.  kernel, constant by file
+EXACT_REGISTERS = {"kv4_prefill.cu": ("kv4_prefill_kernel", "kLaunchRegs")}
+
+
+def registers_of(ptxas: str, kernel: str) -> dict:
+    """{variant: registers} of a kernel, from what `ptxas -v` printed."""
+    found, name = {}, None
+    for line in ptxas.splitlines():
+        m = re.search(r"Compiling entry function '(\w+)'", line)
+        name = m.group(1) if m else name
+        m = re.search(r"Used (\d+) registers", line)
+        if m and name and kernel in name:
+            found[name] = int(m.group(1))
+    return found
+
+
+def check_registers(src: str, text: str, ptxas: str) -> None:
+    """Fails the build where a kernel of EXACT_REGISTERS was not compiled to its source's count."""
+    kernel, constant = EXACT_REGISTERS[os.path.basename(src)]
+    want = int(re.search(constant + r" = (\d+)", text).group(1))
+    found = registers_of(ptxas, kernel)
+    wrong = {k: v for k, v in found.items() if v != want}
+    if wrong or not found:
+        raise RuntimeError(f"{src}: {kernel} needs {want} registers in every variant ({constant} and the shares of its "
+                           f"roles), the compiler gave {wrong or 'no figures'}")
+
+
 def _compile(src: str, extra) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+    exact = os.path.basename(src) in EXACT_REGISTERS
+    if exact and not extra:
+        extra = ["-Xptxas", "-v"]
     cmd = [nvcc(), *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+    if exact:
+        with open(src) as f:
+            check_registers(src, f.read(), r.stderr)
     if r.stderr.strip() and "ptxas info" in r.stderr:
         with open(obj + ".ptxas.txt", "w") as f:
             f.write(r.stderr)

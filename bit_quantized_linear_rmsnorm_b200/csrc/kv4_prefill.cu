@@ -57,6 +57,7 @@
 // Every wait is bounded; if one runs out the kernel records BQ_ERR_TIMEOUT,
 // lets its copies and products end (bounded again) and finishes.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kv4_attention.cuh"
@@ -1209,12 +1210,16 @@ cudaError_t launch_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &
     static SmemOptIn opt_in;
     cudaError_t e = smem_opt_in(opt_in, dev, reinterpret_cast<const void *>(kern), static_cast<size_t>(C::SMEM));
     if (e != cudaSuccess) return e;
-    // the register split of the roles adds up to what a CTA is launched with
-    static const int regs = [&] {
+    // The register split of the roles adds up to what a CTA is launched with.  The build checks that (_build.py); a
+    // library that was built some other way is refused here, since its warps would wait for registers for ever.
+    static std::atomic<bool> checked{false};
+    if (!checked.load(std::memory_order_relaxed)) {
         cudaFuncAttributes f = {};
-        return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        e = cudaFuncGetAttributes(&f, kern);
+        if (e != cudaSuccess) return e;  // (asked again by the next call)
+        if (f.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        checked.store(true, std::memory_order_relaxed);
+    }
     const unsigned grid = static_cast<unsigned>(std::min(dev.num_sms, kKv4MaxSms));
     const Kv4Ws ws = kv4_workspace(a.workspace);
     kern<<<grid, kPThreads, C::SMEM, s>>>(a, ws, dev.status);

@@ -293,3 +293,14 @@ def test_caps_of_every_size(D, G, n):
     for cap in (64.0, 200.0):  # with what else changes a score
         run_attention(s, q, [n, n], softcap=cap, slopes=2.0 ** -np.arange(1.0, 5.0), window=33)
     status_ok()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(slopes=1), dict(softcap=500.0)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_every_variant_is_launched(D, G, dtype, kw):
+    """Type, layout, what changes a score, and the number of columns (4, 12, 20, 160) choose the kernel's variant."""
+    kw = extras(kw, 4)
+    s = Setup([70], 1, D, G, 32, seed=32).fill()
+    for n in (1, 3, 5, 40):
+        run_attention(s, query(s, n, 4, dtype), [n], **kw)
