@@ -481,7 +481,7 @@ def _kv4_cache(cache: torch.Tensor, D: int, group_size: int, *tables):
     """(pages, page stride, page size, kv_heads) of a cache, after checking it and the integer tables that go with it.
 
     (A decode step is a few microseconds long, so these checks ask a tensor for as little as they can.)"""
-    if cache.dtype is not torch.uint8 or cache.dim() != 3 or group_size < 1 or D % group_size != 0:
+    if cache.dtype is not torch.uint8 or cache.dim() != 3 or group_size < 1 or D < 1 or D % group_size != 0:
         raise ValueError("expected a uint8 cache [pages, kv_heads, page_bytes] and a group_size that divides head_dim")
     pages, H, nbytes = cache.shape
     pstride, hstride, inner = cache.stride()
@@ -493,7 +493,7 @@ def _kv4_cache(cache: torch.Tensor, D: int, group_size: int, *tables):
     if dev < 0:
         raise ValueError("the cache must be on a GPU")
     for t in tables:
-        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev or
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev or t.dim() == 0 or
                               (t.stride(-1) != 1 and t.shape[-1] > 1)):
             raise ValueError("block_table, lengths and offsets must be int32 on the cache's device, dense along a row")
     return pages, (pstride if pages > 1 else H * nbytes), page, H
@@ -519,6 +519,8 @@ def _kv4_strides(t: torch.Tensor):
 
 def _kv4_call(dev: int, fn, stream, *args):
     """fn(*args, stream handle) with device `dev` current (the library launches on the current device)."""
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError("the stream must be one of the cache's device")
     if dev == torch.cuda.current_device():
         return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     with torch.cuda.device(dev):

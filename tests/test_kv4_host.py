@@ -189,6 +189,37 @@ def test_allocations_follow_the_stream(monkeypatch):
             assert [m[0] for m in made] == [name] * count and given == [stream and name]
 
 
+def test_binding_refuses_empty_heads_and_single_numbers():
+    """No head of 0 elements, no table that is a single number, no stream of another device: a ValueError each."""
+    class Elsewhere:
+        cuda_stream, device_index = 0, 1
+
+    nbytes = ref.page_bytes(16, 64, 64)
+    cache = on_device(torch.zeros(3, 2, nbytes, dtype=torch.uint8))
+    table, lens = (on_device(torch.ones(s, dtype=torch.int32)) for s in ((2, 1), (2,)))
+    cu = on_device(torch.tensor([0, 1, 2], dtype=torch.int32))
+    single = on_device(torch.tensor(1, dtype=torch.int32))
+    q, none = (on_device(torch.zeros(s).bfloat16()) for s in ((2, 2, 64), (2, 2, 0)))
+    bad = [
+        lambda: bq.bq_kv4_write(none, none, cache, table, lens, 64),
+        lambda: bq.bq_kv4_attention(none, cache, table, lens, 64),
+        lambda: bq.bq_kv4_read(cache, table, cu, 2, 0, 64),
+        lambda: bq.bq_kv4_read(cache, table, cu, 2, -64, 64),
+        lambda: bq.bq_kv4_write(q, q, cache, single, lens, 64),
+        lambda: bq.bq_kv4_write(q, q, cache, table, single, 64),
+        lambda: bq.bq_kv4_attention(q, cache, table, single, 64),
+        lambda: bq.bq_kv4_attention(q, cache, table, lens, 64, cu_q=single),
+        lambda: bq.bq_kv4_read(cache, table, single, 2, 64, 64),
+        lambda: bq.bq_kv4_read(cache, table, cu, 2, 64, 64, starts=single),
+        lambda: bq.bq_kv4_write(q, q, cache, table, lens, 64, stream=Elsewhere()),
+        lambda: bq.bq_kv4_read(cache, table, cu, 2, 64, 64, k=q, v=q, stream=Elsewhere()),
+        lambda: bq.bq_kv4_attention(q, cache, table, lens, 64, out=q, workspace=q, stream=Elsewhere()),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+
+
 # ------------------------------------------------------------------ pins of the yardstick
 def test_quantize_by_hand():
     # minimum 0, maximum 15: step 1, so a value is its own code and k + 1/2 goes to the even neighbour
