@@ -304,3 +304,29 @@ def test_every_variant_is_launched(D, G, dtype, kw):
     s = Setup([70], 1, D, G, 32, seed=32).fill()
     for n in (1, 3, 5, 40):
         run_attention(s, query(s, n, 4, dtype), [n], **kw)
+
+
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_what_lies_in_place_of_a_bad_page_does_not_count(D, G):
+    """Small values beside a NaN token and a page that is not there, after items with very large ones: rows that see
+    neither are as exact as ever, though the missing page's place still holds what an earlier tile left."""
+    lens = [300, 96] * 8
+    s = Setup(lens, 1, D, G, 16, seed=33)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            k, v = s.rng.standard_normal((2, 1, D)).astype(np.float32)
+            v = v * 1.5e4 if n == 300 else v * 2.0 ** -18
+            s.host.put(*s.place(b, t), k, np.full_like(v, np.nan) if n == 96 and t == 78 else v)
+    counts = [40] * 16
+    q = query(s, sum(counts), 4, "bf16")
+    table = s.table.copy()
+    table[1::2, 5] = -1  # positions 80 .. 95
+    out = bq.bq_kv4_attention(q, s.cuda(), dev(table), dev(lens), G)
+    assert bq.bq_device_status()[0] == bq.BQ_ERR_INVALID_ARG
+    want, _, tol = ref.attention(q.double().cpu().numpy(), s.host, s.table, lens, offsets(counts), D ** -0.5)
+    got = out.double().cpu().numpy()
+    for b in range(1, 16, 2):
+        rows = slice(40 * b, 40 * b + 22)  # positions 56 .. 77
+        assert np.isnan(got[40 * b + 22: 40 * b + 40]).all()
+        bound = tol[rows] + 2.0 ** -8 * (np.abs(want[rows]) + tol[rows])
+        assert (np.abs(got[rows] - want[rows]) <= bound).all()
