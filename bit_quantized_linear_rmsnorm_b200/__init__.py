@@ -581,7 +581,7 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
                      slopes=None, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of q [T, q_heads, D] over a 4-bit cache: each sequence's rows stand at the end of its
     seq_lens tokens.  cu_q [batch + 1] gives the rows of each sequence (None: T / batch each), max_q the most rows of
-    one (None: T).  Returns out [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given.  What is not given
+    one (None: T; which kernel runs goes by it, so with cu_q say it where every sequence has few).  Returns out [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given.  What is not given
     (out, the workspace) is allocated on `stream`; calls that run at the same time need a workspace each."""
     dev = cache.get_device()
     if q.dim() != 3 or q.get_device() != dev or q.dtype not in _DTYPE or (q.numel() and q.stride(2) != 1):

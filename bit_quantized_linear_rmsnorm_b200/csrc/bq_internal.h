@@ -272,7 +272,18 @@ struct Kv4AttnArgs {
 size_t kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev);
 cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &dev);
-constexpr int64_t kKv4FewColumns = 24;  // rows of a sequence * query heads of a key head up to which the cache bounds
+// Columns (rows of a sequence * query heads of a key head) up to which the
+// few-row kernel runs, in blocks of up to 24 that each read and unpack the
+// cache again; beyond it the many-row kernel, whose tiles of 128 cost the same
+// however few of their columns are used.  Device times, us, few | many rows,
+// 8 heads of 128 (bf16), at 24, 48, 72 and 96 columns:
+//   32 sequences of up to 2500    52|91   65|93   93|103  106|103
+//   1 of 8192                     22|39   31|40   35|42    40|44
+//   1 of 131072                   80|198 142|200 199|200  258|202
+//   64 of up to 8192             157|375 260|425 306|407  382|442
+//   the first with groups of 64   65|130  78|115 117|134  127|139
+//   the first, heads of 64        37|76   50|81   71|86    71|82
+constexpr int64_t kKv4FewColumns = 72;
 
 // Grouped INT4 linear.
 size_t linear_w4_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t group_size);

@@ -825,7 +825,7 @@ cudaError_t launch_decode(const Kv4AttnArgs &a, cudaStream_t s, const DevInfo &d
 }  // namespace
 
 size_t kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
-    // two slots for each CTA: three per SM with 8 columns, two with 24, or, for many rows, one with 256
+    // two slots for each CTA: three per SM with 8 columns, two with 24 (of a block), or, for many rows, one with 256
     const int64_t cols = total * (q_heads / kv_heads) > kKv4FewColumns ? 256 : 48;
     return kKv4MaxCtas * sizeof(Kv4Partial) + 2 * kKv4MaxSms * static_cast<size_t>(cols * (head_dim + 4)) * 4;
 }

@@ -567,7 +567,9 @@ size_t bq_kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t 
  * (multiples of 16 bytes), 16-byte aligned; q_heads a multiple of kv_heads,
  * query head h reading key head h / (q_heads / kv_heads).  max_q: at least the
  * rows of the longest sequence (rows behind it are left out); ignored where
- * cu_q is NULL.  scale finite; softcap finite and >= 0 (0: none); window >= 0
+ * cu_q is NULL.  Up to 72 columns (max_q * q_heads / kv_heads) the kernel for
+ * few rows runs, beyond that the one for many, which takes two to four times as
+ * long for one row a sequence: a max_q of `total` costs that.  scale finite; softcap finite and >= 0 (0: none); window >= 0
  * (0: none); slopes fp32 [q_heads] or NULL.  out: dense [total][q_heads][D] of
  * dtype, 16-byte aligned.  lse: fp32 [total][q_heads] or NULL.
  * workspace: at least bq_kv4_attention_workspace_bytes(total, ...) bytes,

@@ -330,3 +330,20 @@ def test_what_lies_in_place_of_a_bad_page_does_not_count(D, G):
         assert np.isnan(got[40 * b + 22: 40 * b + 40]).all()
         bound = tol[rows] + 2.0 ** -8 * (np.abs(want[rows]) + tol[rows])
         assert (np.abs(got[rows] - want[rows]) <= bound).all()
+
+
+@pytest.mark.parametrize("D,G,share", [(64, 64, 1), (128, 64, 4), (128, 128, 3), (64, 64, 24), (128, 128, 73)])
+def test_columns_on_either_side_of_what_is_chosen(D, G, share):
+    """Blocks of 24 columns of the few-row kernel, whole and begun, inside and between rows, up to its last column; and
+    the many-row kernel's first."""
+    s = Setup([200, 0, 140, 31], 2, D, G, 16, seed=34).fill()
+    for cols in (9, 24, 25, 48, 49, 71, 72, 73, 96):
+        if cols % share == 0 or share in (1, cols):
+            n = cols // share
+            counts = [n, 1, max(n // 2, 1), n]
+            run_attention(s, query(s, sum(counts) + 1, 2 * share, "f16"), counts, rows_behind=1)
+            run_attention(s, query(s, sum(counts) + 1, 2 * share, "bf16"), counts, rows_behind=1, window=20, softcap=30.0)
+    # cut into parts
+    s = Setup([4000], 1, D, G, 64, seed=35).fill()
+    for n in {max(1, 72 // share), max(1, 40 // share)}:
+        run_attention(s, query(s, n, share, "f16"), [n])
