@@ -347,3 +347,44 @@ def test_columns_on_either_side_of_what_is_chosen(D, G, share):
     s = Setup([4000], 1, D, G, 64, seed=35).fill()
     for n in {max(1, 72 // share), max(1, 40 // share)}:
         run_attention(s, query(s, n, share, "f16"), [n])
+
+
+def test_pages_far_into_a_large_pool():
+    """A pool of 5 GiB: byte offsets beyond 32 bits, signed or not, in the write, the read and both attention kernels."""
+    D, G, page, H = 128, 64, 64, 2
+    nbytes = ref.page_bytes(page, D, G)
+    pages = (5 << 30) // (H * nbytes)
+    s = Setup([150, 70], H, D, G, page, seed=36).fill()
+    far = (2 ** 31 // (H * nbytes) + 1, 2 ** 32 // (H * nbytes), 2 ** 32 // (H * nbytes) + 1, pages - 1, pages - 2, 3, 0)
+    table = np.full_like(s.table, -1)
+    pool = torch.zeros((pages, H, nbytes), dtype=torch.uint8, device="cuda")
+    here = torch.from_numpy(s.host.pool).cuda()
+    at = 0
+    for b, n in enumerate(s.lens):
+        for i in range(-(-n // page)):
+            table[b, i] = far[at]
+            pool[far[at]] = here[int(s.table[b, i])]
+            at += 1
+    for counts in ([1, 1], [90, 40]):
+        cu = offsets(counts)
+        q = query(s, sum(counts), 4, "bf16")
+        out = bq.bq_kv4_attention(q, pool, dev(table), dev(s.lens), G, cu_q=dev(cu), max_q=max(counts))
+        check_attention(s, out, None, q, cu, D ** -0.5)
+    cu = dev(offsets(s.lens))
+    k, v = bq.bq_kv4_read(pool, dev(table), cu, 220, D, G, out_dtype=torch.float32)
+    for which, got in ((0, k), (1, v)):
+        want = np.concatenate([s.host.values(which, s.table[b], n, np.float32) for b, n in enumerate(s.lens)])
+        assert np.array_equal(got.cpu().numpy(), want)
+    other = torch.zeros_like(pool)
+    bq.bq_kv4_write(k, v, other, dev(table), dev(s.lens), G, cu_q=cu)
+    k2, v2 = bq.bq_kv4_read(other, dev(table), cu, 220, D, G, out_dtype=torch.float32)
+    # (a group's smallest and largest value are kept to half a step of fp16's, the others to half a step more)
+    for a, b in ((k, k2), (v, v2)):
+        span = a.unflatten(-1, (-1, G))
+        span = (span.amax(-1) - span.amin(-1)).repeat_interleave(G, -1)
+        assert ((a - b).abs() <= span / 15 * 0.51 + a.abs() * 2.0 ** -10 + 1e-6).all()
+    used = torch.zeros(pages, dtype=torch.bool, device="cuda")
+    used[torch.from_numpy(table[table >= 0].astype(np.int64)).cuda()] = True
+    touched = torch.cat([(x != 0).flatten(1).any(1) for x in other.split(4096)])
+    assert torch.equal(touched, used)
+    status_ok()
