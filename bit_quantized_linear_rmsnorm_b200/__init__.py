@@ -478,7 +478,8 @@ def bq_kv4_page_bytes(page_size: int, head_dim: int, group_size: int) -> int:
 
 
 def _kv4_cache(cache: torch.Tensor, D: int, group_size: int, *tables):
-    """(pages, page stride, page size, kv_heads) of a cache, after checking it and the integer tables that go with it.
+    """(pages, page stride, page size, kv_heads) of a cache, after checking it and the integer tables that go with it
+    (whose shapes _kv4_batch has checked).
 
     (A decode step is a few microseconds long, so these checks ask a tensor for as little as they can.)"""
     if cache.dtype is not torch.uint8 or cache.dim() != 3 or group_size < 1 or D < 1 or D % group_size != 0:
@@ -493,7 +494,7 @@ def _kv4_cache(cache: torch.Tensor, D: int, group_size: int, *tables):
     if dev < 0:
         raise ValueError("the cache must be on a GPU")
     for t in tables:
-        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev or t.dim() == 0 or
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev or
                               (t.stride(-1) != 1 and t.shape[-1] > 1)):
             raise ValueError("block_table, lengths and offsets must be int32 on the cache's device, dense along a row")
     return pages, (pstride if pages > 1 else H * nbytes), page, H
@@ -519,12 +520,16 @@ def _kv4_strides(t: torch.Tensor):
 
 def _kv4_call(dev: int, fn, stream, *args):
     """fn(*args, stream handle) with device `dev` current (the library launches on the current device)."""
-    if stream is not None and getattr(stream, "device_index", dev) != dev:
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif getattr(stream, "device_index", dev) != dev:
         raise ValueError("the stream must be one of the cache's device")
+    else:
+        handle = stream.cuda_stream
     if dev == torch.cuda.current_device():
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+        return fn(*args, handle)
     with torch.cuda.device(dev):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+        return fn(*args, handle)
 
 
 def bq_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -537,10 +542,10 @@ def bq_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_ta
             v.get_device() != dev or (k.numel() and (k.stride(2) != 1 or v.stride(2) != 1)):
         raise ValueError("expected k and v [T, kv_heads, D] of one type, dense along D, on the cache's device")
     T, H, D = k.shape
+    B, ld, width = _kv4_batch(block_table, seq_lens, cu_q)
     pages, pstride, page, Hc = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
     if H != Hc or k.dtype not in _DTYPE:
         raise ValueError("k and v must have the cache's heads and a supported type")
-    B, ld, width = _kv4_batch(block_table, seq_lens, cu_q)
     kt, kh = _kv4_strides(k)
     vt, vh = _kv4_strides(v)
     st = _kv4_call(dev, lib().bq_kv4_write, stream, k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], T, H, D, kt, kh, vt, vh,
@@ -554,13 +559,16 @@ def bq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, cu_len: torch.Te
                 group_size: int, starts=None, out_dtype=torch.bfloat16, k=None, v=None, stream=None):
     """(k, v) [total, kv_heads, D]: positions starts[b] + j (starts None: 0) of each sequence, its rows cu_len[b] up
     to cu_len[b + 1].  Outputs that are not given are allocated on `stream`."""
-    pages, pstride, page, H = _kv4_cache(cache, head_dim, group_size, block_table, cu_len, starts)
     B, ld, width = _kv4_batch(block_table, None, cu_len, starts)
+    pages, pstride, page, H = _kv4_cache(cache, head_dim, group_size, block_table, cu_len, starts)
     shape, dev = (total, H, head_dim), cache.get_device()
     if k is None:
         k = _empty(shape, out_dtype, cache.device, stream)
     if v is None:
-        v = _empty(shape, k.dtype, cache.device, stream)
+        if stream is None:
+            v = torch.empty_like(k)
+        else:
+            v = _empty(shape, k.dtype, cache.device, stream)
     if k.shape != shape or v.shape != shape or k.dtype is not v.dtype or k.dtype not in _DTYPE or \
             not (k.is_contiguous() and v.is_contiguous()) or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("k and v must be dense [total, kv_heads, head_dim] of one type on the cache's device")
@@ -581,14 +589,15 @@ def bq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
                      slopes=None, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of q [T, q_heads, D] over a 4-bit cache: each sequence's rows stand at the end of its
     seq_lens tokens.  cu_q [batch + 1] gives the rows of each sequence (None: T / batch each), max_q the most rows of
-    one (None: T; which kernel runs goes by it, so with cu_q say it where every sequence has few).  Returns out [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given.  What is not given
-    (out, the workspace) is allocated on `stream`; calls that run at the same time need a workspace each."""
+    one (None: T; which kernel runs goes by it, so with cu_q say it where every sequence has few).  Returns out
+    [T, q_heads, D]; `lse` (fp32 [T, q_heads]) is filled where given.  What is not given (out, the workspace) is
+    allocated on `stream`; calls that run at the same time need a workspace each."""
     dev = cache.get_device()
     if q.dim() != 3 or q.get_device() != dev or q.dtype not in _DTYPE or (q.numel() and q.stride(2) != 1):
         raise ValueError("expected q [T, q_heads, D], dense along D, on the cache's device")
     T, Hq, D = q.shape
-    pages, pstride, page, H = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
     B, ld, width = _kv4_batch(block_table, seq_lens, cu_q)
+    pages, pstride, page, H = _kv4_cache(cache, D, group_size, block_table, seq_lens, cu_q)
     if out is None:
         out = _empty((T, Hq, D), q.dtype, q.device, stream)
     elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != dev or not out.is_contiguous():
