@@ -21,11 +21,16 @@
 // so 8 columns carry the query rows and heads that share a key head, and p
 // moves from one product to the next by two 8 x 8 register transposes.
 //
-// Roundings.  q is scaled by a power of two into fp16 (exact for bf16 and fp16
-// values within 2^-29 of the row's largest).  p * s_v is rounded once to fp16,
-// the type of the instruction; the sums that go with it (the divisor, and
-// the minima's term) are taken of the same rounded weights, so the rounding
-// acts as a relative error of a weight, 2^-11 at most, and cancels for a
+// Roundings.  q is scaled by a power of two into fp16, odd elements 2^4 lower:
+// exact for bf16 values within 2^-27 of the row's largest, fp16 values within
+// 2^-24; what is smaller is off by 2^-35 of it at most.  p * s_v is rounded
+// once to fp16, the type of the instruction (a second half of it would double
+// the products with the values, and a bf16 result's error, 0.0017 of the
+// largest, is that of a 32-bit computation as it is; fp16 results have 0.0003
+// where that has 0.0002); the sums that go with it (the divisor, and the
+// minima's term, and with them lse) are taken of the same rounded weights, so
+// the rounding acts as a relative error of a weight, 2^-11 at most (weights
+// below 2^-21 of the largest: 2^-32 of that one), and cancels for a
 // single token.  (A step far below the others' can leave fp16's normal range
 // with its weight: such a weight counts in the sums as it is.)
 // Running maximum, sums and products are fp32.  The maximum is
@@ -33,7 +38,8 @@
 // are; it is raised only when a score passes it by 2^8 (the weights then stay
 // below 2^15), so most tiles need no shuffles and no rescaling.
 //
-// Work.  The tiles (32 tokens of one key head and column block) of the whole
+// Work.  Up to 72 columns (bq_internal.h has the measurements), in blocks of
+// 8, 16 or 24.  The tiles (32 tokens of one key head and column block) of the whole
 // batch, and kStart tiles' worth for beginning an item, are one list, cut into
 // equal shares for the CTAs, whatever the lengths are: three CTAs per SM (two
 // where more columns take the registers), 4 warps each, every warp with a ring
@@ -43,7 +49,7 @@
 // programmatic dependent, joins them.
 //
 // What bounds it: DRAM traffic is the cache read once (321 MB for 64 ragged
-// sequences of up to 8192 tokens, 8 heads of 128), but at 98 us (50% of the
+// sequences of up to 8192 tokens, 8 heads of 128), but at 96 to 98 us (50% of the
 // measured copy bandwidth) it is the issue of instructions: about 720 for a
 // tile, of which 192 bring codes into registers, at 57% of the issue slots,
 // the rest being fixed latencies of 12 warps.  Measured against this split:

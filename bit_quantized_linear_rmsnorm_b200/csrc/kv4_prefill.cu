@@ -12,14 +12,20 @@
 // so that the output is (2^e0 O + 2^e1 L_m) / L_1: the divisor and the middles'
 // term are sums of the same rounded weights w as the codes' term, and the
 // rounding of a weight (2^-11 at most) changes how much a token counts, never
-// what it stands for.  1/mu is a pair of fp16 (22 bits); so is a middle, whose
+// what it stands for.  (fp16 is the type of the instruction; two products for
+// one would take fp16 results from a relative error of 0.00023 to 0.00021, bf16
+// results from 0.0017 nowhere.  Weights below 2^-12 of a row's largest may keep fewer bits: they
+// are off by 2^-23 of that one at most.)  1/mu, which the divisor's sum takes
+// as an operand of the same product, is a pair of fp16 (22 bits, a relative
+// error of 2^-23 beside the sum's own); so is a middle, whose
 // second half is held times 2^14, so that one far below the largest keeps its
 // bits (to 2^-41 of the largest; 2^-27 without that, which a row that sees only
 // small ones would notice).  The
 // values' codes are taken from the middle because the tensor core's additions
 // round toward zero: sums of 0..15 drift with every step, and what is left of
 // them after the minima's term is small (0.0029 against 0.0017 relative error
-// over 9000 tokens, the latter being bf16's own; now 0.0017).
+// over 9000 tokens, the latter being bf16's own; now 0.0017).  It is paid for
+// with time: 2048 rows after 8192 took 484 us before, 503 us after it.
 // The exponents e0, e1 follow the largest step and middle so far, and the sums
 // are rescaled when they move; where steps differ by more than 2^9, part of a
 // step's exponent goes from the weight into the codes ((c_v - 8) 2^k).  A code
@@ -44,7 +50,7 @@
 // kernel adds up what was cut.
 //
 // What bounds it (2048 rows of 32 heads after 8192 tokens, 8 key heads of 128:
-// 503 us, 615 TFLOP/s, tensor pipe active 31%): a tile's softmax (about 2700
+// 495 us, 625 TFLOP/s, tensor pipe active 31%): a tile's softmax (about 2700
 // cycles while the other tile's runs too) and its two products (880 cycles, and
 // 900 to hand over) follow one another, since its weights take the place of its
 // scores; issue slots are 45% full, the exponentials' unit 29%, shared memory
@@ -988,8 +994,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prefill_kernel(const Kv4Attn
                         } else {
                             uint32_t mult = 0, less = 0, mult16 = 0, less16 = 0;  // 2^k, -1032 2^k, 2^(k - 4), -72 2^k
                             if (fit) {
-                                // a step far below e0's takes part of its exponent into the weight; what would
-                                // leave fp16 even so (below 2^-20 of the largest step) counts as 0
+                                // a step far below e0's takes part of its exponent into the weight (the codes
+                                // reach down to 2^-24, 16 times a code's 2^k); where 1 / mu would leave fp16 even
+                                // so, at steps below 2^-34 of the largest, the codes count as their middle
                                 const int k = max(exp_of(x.x) - e0, -20);
                                 mu = x.x * pow2i(-k - e0);
                                 inv = rcp(mu);

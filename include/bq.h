@@ -574,11 +574,13 @@ size_t bq_kv4_attention_workspace_bytes(int64_t total, int64_t q_heads, int64_t 
  * dtype, 16-byte aligned.  lse: fp32 [total][q_heads] or NULL.
  * workspace: at least bq_kv4_attention_workspace_bytes(total, ...) bytes,
  * 256-byte aligned; it carries nothing from one call to the next, but two
- * calls that run at the same time need one each.  A weight of the softmax is
- * rounded once to 11 bits, in numerator and divisor alike (and, for sequences
- * of few rows, in lse, which it moves by 2^-11 at most); everything else is
- * summed in fp32, of the stored codes as they are.  The result does not depend
- * on timing: the same call gives the same bits.
+ * calls that run at the same time need one each.  A weight of the softmax,
+ * times the value's step, is rounded once to fp16: to 11 bits, in numerator
+ * and divisor alike (and, for sequences of few rows, in lse, which it moves by
+ * 2^-11 at most), or, below 2^-12 of the row's largest, to 2^-23 of that one.
+ * Everything else is summed in fp32, of the stored codes as they are.  Scores
+ * are fp32: |scale| times a row's largest |q| has to stay below 2^100.  The
+ * result does not depend on timing: the same call gives the same bits.
  */
 bq_status bq_kv4_attention(const void *q, bq_dtype dtype, int64_t total, int64_t q_heads, int64_t head_dim,
                            int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_q, int64_t max_q,
